@@ -461,6 +461,101 @@ int attn_decode_sparse_fp8(const kvattn_bf16* q, const uint8_t* latent_fp8, cons
                            float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                            void* stream);
 
+/* ---- paged cache: ragged batches of new tokens, in bf16 or FP8 -------------------
+ * "注意力机制进化史" (the cache append: new k, v behind layer_past) and "注意力变体与 MoE"
+ * (GQA attention(), the lower-triangular mask, decode reading every cached row), for a
+ * server's batch: sequences of any lengths whose cache rows lie in pages, each bringing
+ * one new token (decode), a few (guessed tokens to check) or a long chunk of a prompt.
+ *
+ * The batch.  n_tokens packed new tokens; sequence b's are cu[b] .. cu[b+1]-1 (cu: device
+ * int32 [B+1]), n_b of them.  seq_lens[b] (device int32 [B]) counts the cached rows of
+ * sequence b WITH its new tokens, so its token i stands at position seq_lens[b] - n_b + i.
+ * The same cu, seq_lens and page table go to the append and to the attention after it.
+ * Tokens behind cu[B] belong to no sequence: nothing is written for them.
+ * The pages.  Row r of sequence b is row r % page_size of page page_table[b][r / page_size]
+ * (device int32 [B][max_pages]; entries past a sequence's last row are never read).
+ * bf16: k_pages, v_pages [n_pages][n_kv_head][page_size][d].  FP8: codes uint8
+ * [n_pages][n_kv_head][page_size][d] and one fp32 scale per row and head
+ * [n_pages][n_kv_head][page_size], d + 4 bytes for a row of K or V; a row stands for
+ * code * scale, quantised by the rule of the FP8 section above (one group of d values).
+ * Device-side checks.  cu outside 0 .. n_tokens or decreasing, or a length outside
+ * [0, max_pages * page_size]: forced into range, KVATTN_STATUS_BAD_LENGTH.  A needed page
+ * outside [0, n_pages): its rows are skipped, KVATTN_STATUS_BAD_INDEX.  Sequences that
+ * overlap in cu, or share a page that an append writes, give undefined values (never
+ * stray accesses).
+ * Limits: 1 <= B <= 1024, head_dim 64 or 128, page_size a power of two in 16 .. 1024,
+ * max_pages * page_size <= 2^30, n_tokens * heads < 2^31, n_pages * n_kv_head < 2^31,
+ * B * n_kv_head <= 16384.
+ * The new tokens' heads are contiguous ([n_head][d]); a token's row begins every
+ * *_stride elements (a multiple of 8, >= heads * d), so that q, k_new and v_new may be
+ * slices of one fused projection.  Calls with n_tokens = 0 do nothing.
+ *
+ * kv_append_paged_rope: k_pages row of each token = RoPE(k_new) at its position
+ * (bit-identical to rope_apply_qk's), v_pages row = v_new.  Tables and pair_style as
+ * kv_append_rope; a position outside [0, max_pos) sets KVATTN_STATUS_BAD_POSITION and
+ * that token is not written.  Nothing else in the pages changes.
+ * kv_append_paged_rope_fp8: the same into an FP8 cache; the key is quantised from its
+ * fp32 rotation (no bf16 step between).  Non-finite inputs are not supported.
+ */
+int kv_append_paged_rope(const kvattn_bf16* k_new, int64_t k_stride, const kvattn_bf16* v_new, int64_t v_stride,
+                         const int32_t* cu, const int32_t* seq_lens, const int32_t* page_table, int B, int n_tokens,
+                         int n_kv_head, int head_dim, int page_size, int max_pages, int n_pages,
+                         kvattn_bf16* k_pages, kvattn_bf16* v_pages, const float* cos_tab, const float* sin_tab,
+                         int max_pos, int pair_style, int32_t* dev_status, void* stream);
+
+int kv_append_paged_rope_fp8(const kvattn_bf16* k_new, int64_t k_stride, const kvattn_bf16* v_new, int64_t v_stride,
+                             const int32_t* cu, const int32_t* seq_lens, const int32_t* page_table, int B,
+                             int n_tokens, int n_kv_head, int head_dim, int page_size, int max_pages, int n_pages,
+                             uint8_t* k_codes, float* k_scales, uint8_t* v_codes, float* v_scales,
+                             const float* cos_tab, const float* sin_tab, int max_pos, int pair_style,
+                             int32_t* dev_status, void* stream);
+
+/*
+ * kv_read_paged_fp8: rows 0 .. seq_lens[b]-1 of every sequence of an FP8 paged cache,
+ * as bf16(code * scale), into contiguous caches k_out, v_out [B][n_kv_head][T_max][d]
+ * (the layout of attn_decode_gqa and attn_prefill_causal); rows past a length are left
+ * as they were.  A length above T_max is clamped to it (KVATTN_STATUS_BAD_LENGTH).
+ */
+int kv_read_paged_fp8(const uint8_t* k_codes, const float* k_scales, const uint8_t* v_codes, const float* v_scales,
+                      const int32_t* page_table, const int32_t* seq_lens, int B, int n_kv_head, int head_dim,
+                      int page_size, int max_pages, int n_pages, int T_max, kvattn_bf16* k_out, kvattn_bf16* v_out,
+                      int32_t* dev_status, void* stream);
+
+/*
+ * attn_chunk_paged: attention of every new token over rows 0 .. its own position of its
+ * sequence (the new tokens' rows having been appended): out [n_tokens][n_head][d] bf16 =
+ * softmax(scale q k^T) v, lse [n_tokens][n_head] fp32 (natural log) or NULL, query head h
+ * reading KV head h / g.  q is rotated by the caller (rope_apply_qk).  A token that sees
+ * no row (seq_lens[b] < n_b, or every page skipped) gets out = 0 and lse = -inf.  Rows
+ * past a sequence's length are never used, whatever they hold; its own rows must be finite
+ * (a non-finite value row can reach the queries that share a key tile with it).
+ * max_q: an upper bound of the chunk lengths that the host knows (<= 0: n_tokens); it
+ * decides how the work is laid out.  A chunk longer than max_q sets
+ * KVATTN_STATUS_BAD_LENGTH and its tokens from max_q on are left unwritten.
+ * workspace: attn_chunk_paged_workspace_bytes(...) bytes for the same B, n_tokens, max_q
+ * and heads, 256-byte aligned; its first KVATTN_DECODE_WS_ZERO_BYTES must be zero before
+ * the first call on it, and every call leaves them zero except one that sets
+ * KVATTN_STATUS_TIMEOUT.  Calls that share a workspace must be ordered.
+ * Supported: g = n_head / n_kv_head in {1, 2, 4, 8, 16, 32, 64}.
+ * attn_chunk_paged_fp8: the same over an FP8 cache.  The codes enter the products exactly;
+ * the keys' scales multiply the scores and the values' scales the weights, in fp32, so the
+ * dequantised rows are never rounded.
+ */
+size_t attn_chunk_paged_workspace_bytes(int B, int n_tokens, int max_q, int n_head, int n_kv_head, int head_dim);
+
+int attn_chunk_paged(const kvattn_bf16* q, int64_t q_stride, const int32_t* cu, const int32_t* seq_lens,
+                     const int32_t* page_table, int B, int n_tokens, int max_q, int n_head, int n_kv_head,
+                     int head_dim, int page_size, int max_pages, int n_pages, const kvattn_bf16* k_pages,
+                     const kvattn_bf16* v_pages, float scale, kvattn_bf16* out, float* lse, void* workspace,
+                     size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+int attn_chunk_paged_fp8(const kvattn_bf16* q, int64_t q_stride, const int32_t* cu, const int32_t* seq_lens,
+                         const int32_t* page_table, int B, int n_tokens, int max_q, int n_head, int n_kv_head,
+                         int head_dim, int page_size, int max_pages, int n_pages, const uint8_t* k_codes,
+                         const float* k_scales, const uint8_t* v_codes, const float* v_scales, float scale,
+                         kvattn_bf16* out, float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                         void* stream);
+
 /* ---- block-level indexer over 4-token groups ----------------------------------
  * "attention" page, "Qwen Sparse Attention (QSA)" §3 ①–④: the visible prefix is
  * cut into groups of 4 tokens; each complete group gets one block key (the mean of

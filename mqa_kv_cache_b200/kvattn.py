@@ -669,3 +669,172 @@ def attn_merge_lse(o_parts, lse_parts, out=None, lse=None, want_lse=True):
         lse = torch.empty((B, H), dtype=torch.float32, device=o_parts.device)
     _check(_lib.attn_merge_lse(_ptr(o_parts), _ptr(lse_parts), n, B, H, d, _ptr(out), _ptr(lse), _stream()))
     return out, lse
+
+
+# ---- paged cache: ragged batches of new tokens, in bf16 or FP8 ----
+
+_append_head = [_vp, _i64, _vp, _i64, _vp, _vp, _vp] + [_i32] * 7
+_lib.kv_append_paged_rope.argtypes = _append_head + [_vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp]
+_lib.kv_append_paged_rope_fp8.argtypes = _append_head + [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp]
+_lib.kv_read_paged_fp8.argtypes = [_vp] * 6 + [_i32] * 7 + [_vp, _vp, _vp, _vp]
+_lib.attn_chunk_paged_workspace_bytes.argtypes = [_i32] * 6
+_lib.attn_chunk_paged_workspace_bytes.restype = _sz
+_chunk_head = [_vp, _i64, _vp, _vp, _vp] + [_i32] * 9
+_lib.attn_chunk_paged.argtypes = _chunk_head + [_vp, _vp, _f32, _vp, _vp, _vp, _sz, _vp, _vp]
+_lib.attn_chunk_paged_fp8.argtypes = _chunk_head + [_vp, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _sz, _vp, _vp]
+
+
+def _paged_need(dev, tensors):
+    """Each (tensor, dtype, name) a contiguous CUDA tensor of that type on device `dev`."""
+    for t, dtype, name in tensors:
+        _need(t, dtype, name)
+        _contig(t, name)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on another device")
+
+
+def _paged_tokens(x, name):
+    """(token stride, device) of packed head vectors [n_tokens, heads, d]: heads contiguous, any
+    token stride (slices of a fused projection).  The device has to be the current one."""
+    _need(x, torch.bfloat16, name)
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [n_tokens, heads, head_dim]")
+    T, H, d = x.shape
+    st, sh, sd = x.stride()
+    if (sd != 1 and d > 1) or (sh != d and H > 1):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    dev = x.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is not on the current device")
+    return (st if T > 1 else H * d), dev
+
+
+def _paged_sizes(cu, seq_lens, page_table, pages, name):
+    """(B, max_pages, n_pages, page_size) from a batch's tensors and its pages [n_pages, Hk, page, d]."""
+    if page_table.dim() != 2 or pages.dim() != 4:
+        raise ValueError(f"page_table must be [B, max_pages] and {name} [n_pages, n_kv_head, page_size, head_dim]")
+    B, max_pages = page_table.shape
+    if seq_lens.numel() != B or (cu is not None and cu.numel() != B + 1):
+        raise ValueError("seq_lens must hold B entries and cu B + 1")
+    return B, max_pages, pages.shape[0], pages.shape[2]
+
+
+def _append_paged(fn, fp8, k_new, v_new, cu, seq_lens, page_table, caches, cos, sin, pair_style, dev_status):
+    k_st, dev = _paged_tokens(k_new, "k_new")
+    v_st, _ = _paged_tokens(v_new, "v_new")
+    i32, f32 = torch.int32, torch.float32
+    rows = torch.uint8 if fp8 else torch.bfloat16
+    _paged_need(dev, [(cu, i32, "cu"), (seq_lens, i32, "seq_lens"), (page_table, i32, "page_table"), (cos, f32, "cos"),
+                      (sin, f32, "sin"), *((t, f32 if n.endswith("scales") else rows, n) for n, t in caches)])
+    pages = caches[0][1]
+    B, max_pages, n_pages, page = _paged_sizes(cu, seq_lens, page_table, pages, caches[0][0])
+    T, Hk, d = k_new.shape
+    for n, t in caches:
+        if t.shape != (pages.shape[:3] if n.endswith("scales") else pages.shape):
+            raise ValueError(f"inconsistent shape of {n}")
+    if v_new.shape != k_new.shape or pages.shape[1] != Hk or pages.shape[3] != d:
+        raise ValueError("inconsistent append shapes")
+    if cos.dim() != 2 or cos.shape[1] * 2 != d or sin.shape != cos.shape:
+        raise ValueError("tables must be [max_pos, d/2]")
+    _check(fn(_ptr(k_new), k_st, _ptr(v_new), v_st, _ptr(cu), _ptr(seq_lens), _ptr(page_table), B, T, Hk, d, page,
+              max_pages, n_pages, *(_ptr(t) for _, t in caches), _ptr(cos), _ptr(sin), cos.shape[0], pair_style,
+              _ptr(dev_status), _stream()))
+
+
+def kv_append_paged_rope(k_new, v_new, cu, seq_lens, page_table, k_pages, v_pages, cos, sin, pair_style=0,
+                         dev_status=None):
+    """Write RoPE(k_new) and v_new ([n_tokens, Hk, d], packed; cu int32 [B + 1]) into the pages of
+    their sequences ([n_pages, Hk, page, d] bf16; page_table int32 [B, max_pages]); seq_lens int32
+    [B] counts the rows with the new tokens, so sequence b's token i goes to row
+    seq_lens[b] - n_b + i, which is also its rotation position."""
+    _append_paged(_lib.kv_append_paged_rope, False, k_new, v_new, cu, seq_lens, page_table,
+                  (("k_pages", k_pages), ("v_pages", v_pages)), cos, sin, pair_style, dev_status)
+
+
+def kv_append_paged_rope_fp8(k_new, v_new, cu, seq_lens, page_table, k_codes, k_scales, v_codes, v_scales, cos, sin,
+                             pair_style=0, dev_status=None):
+    """kv_append_paged_rope into an FP8 cache: E4M3 codes uint8 [n_pages, Hk, page, d] and one fp32
+    scale per row and head [n_pages, Hk, page], quantised as they are written."""
+    _append_paged(_lib.kv_append_paged_rope_fp8, True, k_new, v_new, cu, seq_lens, page_table,
+                  (("k_codes", k_codes), ("k_scales", k_scales), ("v_codes", v_codes), ("v_scales", v_scales)),
+                  cos, sin, pair_style, dev_status)
+
+
+def kv_read_paged_fp8(k_codes, k_scales, v_codes, v_scales, page_table, seq_lens, k_out, v_out, dev_status=None):
+    """Rows 0 .. seq_lens[b]-1 of an FP8 paged cache as bf16(code * scale) into the contiguous
+    caches k_out, v_out [B, Hk, T_max, d] (rows past a length stay as they were)."""
+    _need(k_out, torch.bfloat16, "k_out")
+    dev = k_out.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError("k_out is not on the current device")
+    _paged_need(dev, [(k_out, torch.bfloat16, "k_out"), (v_out, torch.bfloat16, "v_out"),
+                      (k_codes, torch.uint8, "k_codes"), (v_codes, torch.uint8, "v_codes"),
+                      (k_scales, torch.float32, "k_scales"), (v_scales, torch.float32, "v_scales"),
+                      (page_table, torch.int32, "page_table"), (seq_lens, torch.int32, "seq_lens")])
+    B, max_pages, n_pages, page = _paged_sizes(None, seq_lens, page_table, k_codes, "k_codes")
+    Bo, Hk, T_max, d = k_out.shape
+    if (v_codes.shape != k_codes.shape or k_scales.shape != k_codes.shape[:3] or v_scales.shape != k_scales.shape
+            or Bo != B or v_out.shape != k_out.shape or k_codes.shape[1] != Hk or k_codes.shape[3] != d):
+        raise ValueError("inconsistent read shapes")
+    _check(_lib.kv_read_paged_fp8(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(page_table),
+                                  _ptr(seq_lens), B, Hk, d, page, max_pages, n_pages, T_max, _ptr(k_out), _ptr(v_out),
+                                  _ptr(dev_status), _stream()))
+
+
+def attn_chunk_paged_workspace_bytes(B, n_tokens, max_q, n_head, n_kv_head, head_dim) -> int:
+    return int(_lib.attn_chunk_paged_workspace_bytes(B, n_tokens, max_q, n_head, n_kv_head, head_dim))
+
+
+def _chunk_paged(fn, fp8, q, cu, seq_lens, page_table, caches, scale, max_q, out, lse, ws, dev_status, want_lse):
+    q_st, dev = _paged_tokens(q, "q")
+    i32, f32 = torch.int32, torch.float32
+    rows = torch.uint8 if fp8 else torch.bfloat16
+    _paged_need(dev, [(cu, i32, "cu"), (seq_lens, i32, "seq_lens"), (page_table, i32, "page_table"),
+                      *((t, f32 if n.endswith("scales") else rows, n) for n, t in caches)])
+    pages = caches[0][1]
+    B, max_pages, n_pages, page = _paged_sizes(cu, seq_lens, page_table, pages, caches[0][0])
+    T, H, d = q.shape
+    Hk = pages.shape[1]
+    for n, t in caches:
+        if t.shape != (pages.shape[:3] if n.endswith("scales") else pages.shape):
+            raise ValueError(f"inconsistent shape of {n}")
+    if pages.shape[3] != d:
+        raise ValueError("inconsistent chunk shapes")
+    if out is None:
+        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _paged_need(dev, [(out, torch.bfloat16, "out")])
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    if lse is not None:
+        _paged_need(dev, [(lse, f32, "lse")])
+        if lse.shape != (T, H):
+            raise ValueError("lse must be [n_tokens, n_head]")
+    elif want_lse:
+        lse = torch.empty((T, H), dtype=f32, device=q.device)
+    max_q = 0 if max_q is None else int(max_q)
+    if ws is None:
+        ws = workspace(attn_chunk_paged_workspace_bytes(B, T, max_q, H, Hk, d), q.device)
+    _check(fn(_ptr(q), q_st, _ptr(cu), _ptr(seq_lens), _ptr(page_table), B, T, max_q, H, Hk, d, page, max_pages,
+              n_pages, *(_ptr(t) for _, t in caches), float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+              _ptr(dev_status), _stream()))
+    return out, lse
+
+
+def attn_chunk_paged(q, cu, seq_lens, page_table, k_pages, v_pages, scale, max_q=None, out=None, lse=None, ws=None,
+                     dev_status=None, want_lse=True):
+    """Attention of every packed new token over rows 0 .. its position of its sequence in a paged
+    bf16 cache that already holds the new tokens' rows: q [n_tokens, H, d] (rotated by the caller),
+    cu int32 [B + 1], seq_lens int32 [B] (rows with the new tokens), page_table int32
+    [B, max_pages], pages [n_pages, Hk, page, d] -> (out [n_tokens, H, d] bf16, lse [n_tokens, H]
+    fp32 or None).  max_q: an upper bound of the chunk lengths known to the host."""
+    return _chunk_paged(_lib.attn_chunk_paged, False, q, cu, seq_lens, page_table,
+                        (("k_pages", k_pages), ("v_pages", v_pages)), scale, max_q, out, lse, ws, dev_status, want_lse)
+
+
+def attn_chunk_paged_fp8(q, cu, seq_lens, page_table, k_codes, k_scales, v_codes, v_scales, scale, max_q=None,
+                         out=None, lse=None, ws=None, dev_status=None, want_lse=True):
+    """attn_chunk_paged over an FP8 cache (kv_append_paged_rope_fp8)."""
+    return _chunk_paged(_lib.attn_chunk_paged_fp8, True, q, cu, seq_lens, page_table,
+                        (("k_codes", k_codes), ("k_scales", k_scales), ("v_codes", v_codes), ("v_scales", v_scales)),
+                        scale, max_q, out, lse, ws, dev_status, want_lse)
