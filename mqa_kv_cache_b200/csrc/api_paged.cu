@@ -1,6 +1,9 @@
 // api_paged.cu -- the extern "C" boundary of the paged-cache operators: argument
 // checks on the host (nothing is launched after a failed one), then the launch.
+#include <cudaTypedefs.h>
+
 #include <cmath>
+#include <mutex>
 
 #include "paged.cuh"
 
@@ -86,6 +89,53 @@ kvattn::PagedBatch batch(const int32_t* cu, const int32_t* seq_lens, const int32
     return p;
 }
 
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link).
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// Map of [z][y][x] with byte strides: bf16 in 128-byte-swizzled boxes 64 wide, or bytes in plain
+// boxes of the whole width; out-of-range parts of a box read as zero.
+int encode_map(const char* name, CUtensorMap* map, const void* base, bool bytes, uint64_t x, uint64_t y, uint64_t z,
+               uint64_t y_stride, uint64_t z_stride, uint32_t box_y, uint32_t box_z)
+{
+    auto fn = encode_fn();
+    if (!fn) return record_error(KVATTN_ERR_CUDA, "%s: cuTensorMapEncodeTiled is unavailable", name);
+    const cuuint64_t dims[3] = {x, y, z}, strides[2] = {y_stride, z_stride};
+    const cuuint32_t box[3] = {bytes ? static_cast<cuuint32_t>(x) : 64u, box_y, box_z}, one[3] = {1, 1, 1};
+    const CUresult r = fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                          const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return record_error(KVATTN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", name, static_cast<int>(r));
+    return KVATTN_OK;
+}
+
+constexpr size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// The chunk workspace: the decode kernels' zero region, then the split blocks' records and partials.
+struct ChunkWorkspace {
+    size_t info = KVATTN_DECODE_WS_ZERO_BYTES, ml, o, total;
+    explicit ChunkWorkspace(int d)
+    {
+        const size_t rows = size_t(2) * kvattn::CHUNK_MAX_CTAS * kvattn::CHUNK_SLOT_ROWS;
+        ml = align_up(info + kvattn::CHUNK_MAX_CTAS * sizeof(int4));
+        o = align_up(ml + rows * sizeof(float2));
+        total = o + rows * d * sizeof(float);
+    }
+};
+
 int append(const char* name, bool fp8, const kvattn_bf16* k_new, int64_t k_stride, const kvattn_bf16* v_new,
            int64_t v_stride, const int32_t* cu, const int32_t* seq_lens, const int32_t* page_table, int B,
            int n_tokens, int n_kv_head, int head_dim, int page_size, int max_pages, int n_pages, void* k_pages,
@@ -166,7 +216,19 @@ int chunk(const char* name, bool fp8, const kvattn_bf16* q, int64_t q_stride, co
     a.d = head_dim;
     a.max_q = max_q <= 0 || max_q > n_tokens ? n_tokens : max_q;
     a.scale = scale;
-    return finish(kvattn::launch_chunk(a, fp8, sms, static_cast<cudaStream_t>(stream)), name);
+    const ChunkWorkspace ws(head_dim);
+    uint8_t* wp = static_cast<uint8_t*>(workspace);
+    a.split_info = reinterpret_cast<int4*>(wp + ws.info);
+    a.part_ml = reinterpret_cast<float2*>(wp + ws.ml);
+    a.part_o = reinterpret_cast<float*>(wp + ws.o);
+    const uint64_t es = fp8 ? 1 : 2, row = head_dim * es, planes = static_cast<uint64_t>(n_pages) * n_kv_head;
+    const uint32_t box = page_size < 128 ? page_size : 128;
+    CUtensorMap mq, mk, mv;
+    if ((rc = encode_map(name, &mq, q, false, head_dim, n_head, n_tokens, head_dim * 2, q_stride * 2, g, 128 / g)) != KVATTN_OK ||
+        (rc = encode_map(name, &mk, k_pages, fp8, head_dim, page_size, planes, row, row * page_size, box, 1)) != KVATTN_OK ||
+        (rc = encode_map(name, &mv, v_pages, fp8, head_dim, page_size, planes, row, row * page_size, box, 1)) != KVATTN_OK)
+        return rc;
+    return finish(kvattn::launch_chunk_tile(a, fp8, mq, mk, mv, sms, static_cast<cudaStream_t>(stream)), name);
 }
 
 }  // namespace
@@ -229,7 +291,7 @@ size_t attn_chunk_paged_workspace_bytes(int B, int n_tokens, int max_q, int n_he
     (void)n_tokens;
     (void)max_q;
     if (B < 1 || n_head < 1 || n_kv_head < 1 || n_head % n_kv_head || head_dim < 1) return 0;
-    return KVATTN_DECODE_WS_ZERO_BYTES;
+    return ChunkWorkspace(head_dim).total;
 }
 
 int attn_chunk_paged(const kvattn_bf16* q, int64_t q_stride, const int32_t* cu, const int32_t* seq_lens,

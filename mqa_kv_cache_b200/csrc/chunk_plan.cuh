@@ -1,0 +1,205 @@
+// chunk_plan.cuh -- how the tensor-core chunk kernel shares its work out.
+//
+// The query rows of (sequence b, KV head) are its tokens times the g heads of the
+// group, token-major, cut into blocks of 256 rows (w = 256 / g tokens).  A block
+// attends to the keys 0 .. (position of its last token), cut into tiles of 128: its
+// unit has that many tiles, each costing 1 where the block has at most 128 rows and 2
+// otherwise.  The costs of all units, in the order (sequence, head, block), form one
+// line of length N; CTA c of G takes the stretch [c N / G, (c + 1) N / G) of it: the
+// tiles whose first cost point lies there.  A unit that crosses a border is finished
+// by the merge from one partial per CTA.  Everything is computed on the device, in
+// closed form per sequence, so the host never waits for lengths.
+#pragma once
+
+#include "paged.cuh"
+
+namespace kvattn {
+
+constexpr int CH_ROWS = 256;  // query rows of a block
+constexpr int CH_KEYS = 128;  // keys of a tile
+
+// sum over i = 1 .. k of the tiles that base + i w keys fill (w a power of two, 4 .. 256).
+__host__ __device__ inline long long chunk_tiles_prefix(int base, int w, int k)
+{
+    int first = 1;  // the blocks before it end at or before row 0
+    if (base < 0) first = -base / w + 1;
+    if (k < first) return 0;
+    const long long n = k - first + 1;
+    const int x0 = base + (first - 1) * w;  // > -w, and x0 + w > 0
+    if (w >= CH_KEYS) {
+        const long long c0 = x0 > 0 ? (x0 + CH_KEYS - 1) / CH_KEYS : -(-x0 / CH_KEYS);
+        return n * c0 + (w / CH_KEYS) * (n * (n + 1) / 2);
+    }
+    const long long m = CH_KEYS / w;                      // blocks per tile of keys
+    const long long r = x0 > 0 ? (x0 + w - 1) / w : 0;    // ceil((x0 + i w) / 128) = ceil((r + i) / m)
+    auto upto = [m](long long x) {                        // sum of ceil(i / m), i = 1 .. x
+        const long long q = x / m;
+        return m * q * (q + 1) / 2 + (x - q * m) * (q + 1);
+    };
+    return upto(r + n) - upto(r);
+}
+
+struct ChunkSeq {
+    int t0, n, take, len;  // packed tokens t0 .. t0 + take - 1 are computed (take = min(n, max_q))
+    __host__ __device__ int base() const { return len - n; }
+    // cost of this sequence's blocks 0 .. k - 1 on one KV head
+    __host__ __device__ long long cost(int k, int w, int g) const
+    {
+        const int full = take / w;
+        if (k <= full) return 2 * chunk_tiles_prefix(base(), w, k);
+        const int rest = take - full * w;
+        const int keys = base() + take;
+        const long long tiles = keys > 0 ? (keys + CH_KEYS - 1) / CH_KEYS : 0;
+        return 2 * chunk_tiles_prefix(base(), w, full) + (rest * g <= CH_ROWS / 2 ? 1 : 2) * tiles;
+    }
+    __host__ __device__ int blocks(int w) const { return (take + w - 1) / w; }
+};
+
+// One unit: a block of query rows of one sequence and KV head.
+struct ChunkUnit {
+    int b, kvh, rb;
+    ChunkSeq s;
+    long long U;     // its first point on the line
+    int rows;        // query rows in use
+    int keys;        // keys that its last token sees
+    int tiles;       // 128-key tiles of them
+    int tiles0;      // tiles that the first 128 rows see
+    int cost;        // points per tile
+};
+
+// Where the batch lies in shared memory: raw offsets and lengths, and the line's prefix
+// per sequence for one KV head.
+struct ChunkPlan {
+    const int* cu;
+    const int* len;
+    const long long* U;  // [B + 1]
+    int B, Hk, g, w, max_q;
+    const PagedBatch* p;
+
+    __host__ __device__ ChunkSeq seq(int b) const
+    {
+        const PagedSeq s = paged_seq(*p, cu[b], cu[b + 1], len[b]);
+        return ChunkSeq{s.t0, s.n, min(s.n, max_q), s.len};
+    }
+    __host__ __device__ long long total() const { return U[B] * Hk; }
+
+    __host__ __device__ void fill(ChunkUnit& u) const  // rows, keys and tiles from b, rb
+    {
+        const int i0 = u.rb * w, left = min(u.s.take - i0, w);
+        u.rows = left * g;
+        u.keys = max(u.s.base() + i0 + left, 0);
+        u.tiles = (u.keys + CH_KEYS - 1) / CH_KEYS;
+        u.cost = u.rows <= CH_ROWS / 2 ? 1 : 2;
+        // the first 128 rows end with token i0 + w / 2 - 1 (g <= 64: w / 2 >= 2); g = 1: w = 256
+        u.tiles0 = u.cost == 1 ? u.tiles : (max(u.s.base() + i0 + w / 2, 0) + CH_KEYS - 1) / CH_KEYS;
+    }
+
+    // the unit holding point x (0 <= x < total())
+    __host__ __device__ ChunkUnit find(long long x) const
+    {
+        int lo = 0, hi = B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (U[mid] * Hk <= x) lo = mid;
+            else hi = mid - 1;
+        }
+        ChunkUnit u;
+        u.b = lo;
+        u.s = seq(lo);
+        const long long per = U[lo + 1] - U[lo];
+        x -= U[lo] * Hk;
+        u.kvh = static_cast<int>(x / per);
+        x -= u.kvh * per;
+        int a = 0, z = u.s.blocks(w) - 1;
+        while (a < z) {
+            const int mid = (a + z + 1) >> 1;
+            if (u.s.cost(mid, w, g) <= x) a = mid;
+            else z = mid - 1;
+        }
+        u.rb = a;
+        u.U = U[lo] * Hk + u.kvh * per + u.s.cost(a, w, g);
+        fill(u);
+        return u;
+    }
+
+    // the next unit with tiles; b = B behind the last one
+    __host__ __device__ void next(ChunkUnit& u) const
+    {
+        u.U += static_cast<long long>(u.cost) * u.tiles;
+        ++u.rb;
+        while (u.b < B) {
+            const int nb = u.s.blocks(w);
+            for (; u.rb < nb; ++u.rb) {
+                fill(u);
+                if (u.tiles > 0) return;
+            }
+            u.rb = 0;
+            if (++u.kvh < Hk && U[u.b + 1] > U[u.b]) continue;
+            u.kvh = 0;
+            do ++u.b;
+            while (u.b < B && U[u.b + 1] == U[u.b]);
+            if (u.b < B) u.s = seq(u.b);
+        }
+    }
+
+    // tiles [tb, te) of u whose first points lie in [lo, hi)
+    __host__ __device__ bool piece(const ChunkUnit& u, long long lo, long long hi, int& tb, int& te) const
+    {
+        const long long a = max(lo, u.U) - u.U, z = min(hi - u.U, static_cast<long long>(u.cost) * u.tiles);
+        tb = static_cast<int>((a + u.cost - 1) / u.cost);
+        te = static_cast<int>((z + u.cost - 1) / u.cost);
+        return tb < te;
+    }
+};
+
+__host__ __device__ __forceinline__ int chunk_owner(long long x, long long N, int G)
+{
+    // c with ceil(c N / G) <= x < ceil((c + 1) N / G)
+    return static_cast<int>((x * G) / N);
+}
+
+__host__ __device__ __forceinline__ long long chunk_start(int c, long long N, int G)
+{
+    return (static_cast<long long>(c) * N + G - 1) / G;
+}
+
+// Block-wide: reads the batch, checks it, and builds the line's prefix.
+__device__ inline void chunk_plan_build(const PagedBatch& p, int Hk, int g, int max_q, int* s_cu, int* s_len,
+                                        long long* s_U, bool report)
+{
+    for (int b = threadIdx.x; b <= p.B; b += blockDim.x) {
+        s_cu[b] = p.cu[b];
+        if (b < p.B) s_len[b] = p.seq_lens[b];
+    }
+    __syncthreads();
+    const int w = CH_ROWS / g;
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+        const PagedSeq s = paged_seq(p, s_cu[b], s_cu[b + 1], s_len[b]);
+        if (report && (s.bad || s.n > max_q)) report_status(p.dev_status, KVATTN_STATUS_BAD_LENGTH);
+        const ChunkSeq q{s.t0, s.n, min(s.n, max_q), s.len};
+        s_U[b + 1] = q.cost(q.blocks(w), w, g);
+    }
+    if (threadIdx.x == 0) s_U[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const int per = (p.B + 31) / 32;
+        const int beg = min(lane * per, p.B), end = min(beg + per, p.B);
+        long long sum = 0;
+        for (int b = beg; b < end; ++b) sum += s_U[b + 1];
+        long long incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        long long run = incl - sum;
+        for (int b = beg; b < end; ++b) {
+            run += s_U[b + 1];
+            s_U[b + 1] = run;
+        }
+    }
+    __syncthreads();
+}
+
+}  // namespace kvattn

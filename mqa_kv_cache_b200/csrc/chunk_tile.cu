@@ -1,0 +1,767 @@
+// chunk_tile.cu -- attention of chunks over a paged KV cache on the tcgen05 tensor
+// cores, for calls whose (sequence, KV head) pairs have many query rows.
+//
+// Method: out = softmax_{j <= p} (scale q . k_j) v_j for the query at position p, query
+// head h reading KV head h / g ("注意力变体与 MoE", GQA attention(); "attention",
+// GroupQueryAttention), one pass over the keys with a running maximum and sum in fp32.
+// The g heads of a group are rows of the same tile, so each K/V row is read once for
+// all of them, and the causal border cuts few tiles.
+//
+// Work: chunk_plan.cuh.  A persistent CTA walks its stretch of (block, key tile)s.  A
+// block of more than 128 rows is two Q tiles that share every K/V tile, so that the
+// softmax of one overlaps the products of the other; a block of at most 128 rows is one
+// Q tile whose even and odd key tiles go to the two softmax groups, each with its own
+// maximum, sum and accumulator, joined from tensor memory at the end.
+//
+// Warps: 0-3 / 4-7 softmax (one thread per query row, its 128 scores in registers),
+// 8 issues the MMAs, 9 loads K/V pages (one box per page and 64-column half, page
+// entries fetched one tile ahead), 10 loads Q, 11 idle.  FP8: warps 12-15 turn the
+// codes of each landed tile into bf16 (exact) in the layout that the MMAs read; the keys'
+// scales multiply the scores and the values' scales the weights, in fp32.
+// TMEM: S0 | S1 | O0 | O1; the weights (bf16) overwrite the first half of their scores
+// and the P V product takes them from there.
+#include "chunk_plan.cuh"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace kvattn {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: the maximum moves only when it grows by more than 2^8
+
+// Degree-4 polynomial for 2^f on [-1/2, 1/2], minimax in relative error (2.7e-6 in fp32
+// Horner form), produced by fit_exp2_poly.py's remez(4): the sums enter an fp32 output
+// (lse), which the degree-3 one's 7.5e-5 would show in.
+__device__ __forceinline__ float2 exp2_poly2(float2 x)
+{
+    x.x = fmaxf(x.x, -125.f);
+    x.y = fmaxf(x.y, -125.f);
+    const float2 t = __fadd2_rn(x, make_float2(kShifter, kShifter));
+    const float2 n = __fadd2_rn(t, make_float2(-kShifter, -kShifter));
+    const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
+    float2 p = __ffma2_rn(make_float2(0.009570102f, 0.009570102f), f, make_float2(0.05591786f, 0.05591786f));
+    p = __ffma2_rn(p, f, make_float2(0.24024744f, 0.24024744f));
+    p = __ffma2_rn(p, f, make_float2(0.6931218f, 0.6931218f));
+    p = __ffma2_rn(p, f, make_float2(0.9999993f, 0.9999993f));
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
+template <int D, bool FP8>
+struct TCfg {
+    static constexpr int HALVES = D / 64;
+    static constexpr int BOX = CH_KEYS * 128;          // 128 rows x 64 bf16
+    static constexpr int TILE = HALVES * BOX;          // a Q, K or V tile
+    static constexpr int CODES = CH_KEYS * D;          // a tile's codes
+    static constexpr int NS = (FP8 ? 3 : 4) * 2 / HALVES;  // bf16 K/V slots
+    static constexpr int LS = FP8 ? 4 / HALVES : 0;        // code slots
+    static constexpr int RING = 8;                     // tiles whose page flags (and scales) are kept
+    static constexpr int THREADS = FP8 ? 512 : 384;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int OFF_LAND = OFF_KV + NS * TILE;
+    static constexpr int OFF_SC = OFF_LAND + LS * CODES;  // [RING][K | V][128] scales
+    static constexpr int OFF_U = OFF_SC + (FP8 ? RING * 2 * CH_KEYS * 4 : 0);
+    static constexpr int OFF_CU = OFF_U + (PAGED_MAX_B + 1) * 8;
+    static constexpr int OFF_LEN = OFF_CU + (PAGED_MAX_B + 1) * 4;
+    static constexpr int OFF_ML = (OFF_LEN + PAGED_MAX_B * 4 + 15) / 16 * 16;  // [2][128] (max, sum)
+    static constexpr int OFF_BAR = OFF_ML + 2 * 128 * 8;
+    // kv_full[NS], kv_empty[NS], land_full[LS], land_empty[LS], q_full, q_empty, s_full[2], p_full[2], pv_done[2], done
+    static constexpr int NBAR = 2 * NS + 2 * LS + 9;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+    static constexpr int SMEM = OFF_MISC + 16 + RING * 4 + 1024;
+    static_assert(SMEM <= 232448, "shared memory");
+    static constexpr uint32_t IDESC_S = umma_idesc_bf16(128, CH_KEYS);
+    static constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D, false, true);
+};
+
+// Four E4M3 codes -> bf16 pairs, exactly: the code's sign, exponent and mantissa bits at
+// bf16's places stand for 2^-120 of its value (subnormal codes are bf16 subnormals then),
+// and the product with 2^120 is exact.
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
+    const uint32_t x = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
+    const uint32_t y = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(lo) : "r"(x), "r"(0x7b807b80u), "r"(0x80008000u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(hi) : "r"(y), "r"(0x7b807b80u), "r"(0x80008000u));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// One row's 128 scores (log2 units after sl2) -> weights to TMEM over the scores; returns their sum.
+// MASKED tiles take every exponential from the hardware unit, where 2^-inf is exactly 0;
+// otherwise a quarter go through the polynomial on the FMA pipe.
+template <bool FP8, bool MASKED>
+__device__ __forceinline__ float row_weights(const uint32_t (&sv)[4][32], float sl2, float mu, uint32_t s_addr,
+                                             const float* vs)
+{
+    const float2 sc2 = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
+    float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[c][2 * i]), __uint_as_float(sv[c][2 * i + 1])),
+                                        sc2, nmu);
+            float2 pr;
+            if (!MASKED && (i & 3) == 0) {
+                pr = exp2_poly2(x);
+            } else {
+                pr.x = fast_exp2(x.x);
+                pr.y = fast_exp2(x.y);
+            }
+            acc[i & 3] = __fadd2_rn(acc[i & 3], pr);
+            if constexpr (FP8) pr = __fmul2_rn(pr, *reinterpret_cast<const float2*>(vs + c * 32 + 2 * i));
+            pk[i] = pack_bf16x2(pr.x, pr.y);
+        }
+        tmem_st16(s_addr + c * 16, pk);
+    }
+    const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+    return (a01.x + a01.y) + (a23.x + a23.y);
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
+    chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, ChunkArgs a)
+{
+    using C = TCfg<D, FP8>;
+    constexpr int NS = C::NS, LS = C::LS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* kv_empty = kv_full + NS;
+    uint64_t* land_full = kv_empty + NS;
+    uint64_t* land_empty = land_full + LS;
+    uint64_t* q_full = land_empty + LS;
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* s_full = q_full + 2;
+    uint64_t* p_full = q_full + 4;
+    uint64_t* pv_done = q_full + 6;
+    uint64_t* done = q_full + 8;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+    volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 16);  // [RING]: groups of 16 keys without a page
+    float* s_sc = reinterpret_cast<float*>(smem + C::OFF_SC);
+    float2* s_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    int* s_cu = reinterpret_cast<int*>(smem + C::OFF_CU);
+    int* s_len = reinterpret_cast<int*>(smem + C::OFF_LEN);
+    long long* s_U = reinterpret_cast<long long*>(smem + C::OFF_U);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&kv_full[i], FP8 ? 4 : 1);
+            mbar_init(&kv_empty[i], 1);
+        }
+        for (int i = 0; i < LS; ++i) {
+            mbar_init(&land_full[i], 1);
+            mbar_init(&land_empty[i], 4);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 2);  // the products' commit, and their issuer
+            mbar_init(&p_full[i], 4);
+            mbar_init(&pv_done[i], 1);
+        }
+        mbar_init(done, 1);
+        *s_abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9 && lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 8) {
+        tmem_alloc(s_tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    pdl_wait();
+    pdl_trigger();
+
+    const PagedBatch& p = a.p;
+    const int w = CH_ROWS / a.g;
+    int gs = 0;
+    while ((1 << gs) < a.g) ++gs;
+    chunk_plan_build(p, a.Hk, a.g, a.max_q, s_cu, s_len, s_U, blockIdx.x == 0);
+    const ChunkPlan plan{s_cu, s_len, s_U, p.B, a.Hk, a.g, w, a.max_q, &p};
+    // tokens that stand before row 0 see nothing (their blocks may have no unit)
+    bool any_blind = false;
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) any_blind |= plan.seq(b).base() < 0;
+    any_blind = __syncthreads_or(any_blind);
+    for (int b = 0; any_blind && b < p.B; ++b) {
+        const ChunkSeq s = plan.seq(b);
+        const int blind = min(-s.base(), s.take);
+        for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+             i < static_cast<long long>(max(blind, 0)) * a.H * (D / 8); i += static_cast<long long>(gridDim.x) * blockDim.x) {
+            const long long row = static_cast<long long>(s.t0) * a.H + i / (D / 8);
+            reinterpret_cast<uint4*>(a.out)[row * (D / 8) + i % (D / 8)] = make_uint4(0, 0, 0, 0);
+            if (a.lse && i % (D / 8) == 0) a.lse[row] = -INFINITY;
+        }
+    }
+    const long long N = plan.total();
+    // every CTA's stretch holds two points at least, so that it owns a tile of each unit it lies in
+    const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), N / 2 > 0 ? N / 2 : 1));
+    const int c = blockIdx.x;
+    const bool active = N > 0 && c < G;
+    long long lo = 0, hi = 0;
+    ChunkUnit u0{};
+    u0.b = p.B;
+    if (active) {
+        lo = chunk_start(c, N, G);
+        hi = chunk_start(c + 1, N, G);
+        u0 = plan.find(lo);
+    }
+    // split units: told to the merge by the CTA of their first tile
+    if (threadIdx.x == 0) a.split_info[c] = make_int4(0, 0, 0, 0);
+
+    if (warp == 9) {
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+        // ===== K/V pages: lane i takes box i of a tile (page, and for bf16 its 64-column half) =====
+        const int bp_shift = min(p.page_shift, 7);  // rows of a box: a page's, 128 at most
+        const int bp = 1 << bp_shift;
+        const int per = FP8 ? 1 : C::HALVES;
+        const int box = lane / per, half = lane % per;
+        const int oob = p.n_pages * a.Hk;  // reads as zeros
+        uint32_t x = 0;  // K and V tiles so far
+        uint32_t it = 0;
+        bool ok = true;
+        for (ChunkUnit u = u0; ok && u.b < p.B && u.U < hi; plan.next(u)) {
+            int tb, te;
+            if (!plan.piece(u, lo, hi, tb, te)) continue;
+            const int32_t* pt = p.page_table + static_cast<long long>(u.b) * p.max_pages;
+            auto entry = [&](int j) {
+                const int row = j * CH_KEYS + (box << bp_shift);
+                return box < (CH_KEYS >> bp_shift) && row < u.keys ? __ldg(pt + (row >> p.page_shift)) : 0;
+            };
+            int e = entry(tb);
+            for (int j = tb; j < te && ok; ++j, ++it) {
+                const int row = j * CH_KEYS + (box << bp_shift);
+                const bool mine = box < (CH_KEYS >> bp_shift) && row < u.keys;
+                const int e_next = j + 1 < te ? entry(j + 1) : 0;
+                const bool bad = mine && (e < 0 || e >= p.n_pages);
+                const uint32_t bads = __ballot_sync(0xffffffffu, bad && half == 0);
+                if (bad && half == 0) report_status(p.dev_status, KVATTN_STATUS_BAD_INDEX);
+                uint32_t groups = 0;
+                if (bads) {
+                    for (int i = 0; i < (CH_KEYS >> bp_shift); ++i)
+                        if (bads >> (i * per) & 1) groups |= ((1u << (bp >> 4)) - 1u) << (i * (bp >> 4));
+                }
+                if (lane == 0) s_bad[it % C::RING] = groups;
+                const int z = bad ? oob : e * a.Hk + u.kvh;
+                const int y = row & ((1 << p.page_shift) - 1);
+                const int boxes = (min(u.keys - j * CH_KEYS, CH_KEYS) + bp - 1) >> bp_shift;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++x) {
+                    if constexpr (FP8) {
+                        const uint32_t slot = x % (LS > 0 ? LS : 1);
+                        if (x >= LS && !(ok = warp_wait(&land_empty[slot], (x / LS - 1) & 1, s_abort))) break;
+                        // with the keys, the scales of both (no copy where the page is bad)
+                        const uint32_t goods = boxes - __popc(bads);
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&land_full[slot], boxes * bp * D + (kv == 0 ? goods * bp * 8 : 0));
+                        __syncwarp();
+                        if (mine) {
+                            tma_load_3d(smem + C::OFF_LAND + slot * C::CODES + (box << bp_shift) * D, kv == 0 ? &tm_k : &tm_v,
+                                        &land_full[slot], 0, y, z);
+                            if (kv == 0 && !bad) {
+                                const long long r = (static_cast<long long>(z) << p.page_shift) + y;
+                                float* dst = s_sc + (it % C::RING) * 2 * CH_KEYS + (box << bp_shift);
+                                bulk_load(dst, a.k_scales + r, bp * 4, &land_full[slot]);
+                                bulk_load(dst + CH_KEYS, a.v_scales + r, bp * 4, &land_full[slot]);
+                            }
+                        }
+                    } else {
+                        const uint32_t slot = x % NS;
+                        if (x >= NS && !(ok = warp_wait(&kv_empty[slot], (x / NS - 1) & 1, s_abort))) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], boxes * bp * 128 * C::HALVES);
+                        __syncwarp();
+                        if (mine)
+                            tma_load_3d(smem + C::OFF_KV + slot * C::TILE + half * C::BOX + (box << bp_shift) * 128,
+                                        kv == 0 ? &tm_k : &tm_v, &kv_full[slot], half * 64, y, z);
+                    }
+                }
+                e = e_next;
+            }
+        }
+        __syncwarp();
+        // copies in flight complete before the CTA leaves (bounded waits)
+        if (lane == 0) {
+            if (!ok) report_status(p.dev_status, KVATTN_STATUS_TIMEOUT);
+            constexpr uint32_t R = FP8 ? LS : NS;
+            uint64_t* full = FP8 ? land_full : kv_full;
+            for (uint32_t i = x > R ? x - R : 0; i < x; ++i) mbar_wait(&full[i % R], (i / R) & 1);
+        }
+    } else if (warp == 10) {
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+        // ===== Q: [128 / g tokens][g heads] boxes, one or two tiles a piece =====
+        if (lane == 0) {
+            int np = 0;
+            for (ChunkUnit u = u0; u.b < p.B && u.U < hi; plan.next(u)) {
+                int tb, te;
+                if (!plan.piece(u, lo, hi, tb, te)) continue;
+                if (np > 0 && (*s_abort || !mbar_wait(q_empty, (np - 1) & 1))) {
+                    *s_abort = 1;
+                    break;
+                }
+                mbar_arrive_expect_tx(q_full, u.cost * C::TILE);
+                for (int t = 0; t < u.cost; ++t)
+#pragma unroll
+                    for (int h = 0; h < C::HALVES; ++h)
+                        tma_load_3d(smem + C::OFF_Q + t * C::TILE + h * C::BOX, &tm_q, q_full, h * 64, u.kvh * a.g,
+                                    u.s.t0 + u.rb * w + t * (w / 2));
+                ++np;
+            }
+            if (np > 0) mbar_wait(q_full, (np - 1) & 1);
+        }
+    } else if (warp == 8) {
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+        // ===== MMA issue (one thread) =====
+        if (lane == 0) {
+            const uint32_t sq = smem_u32(smem + C::OFF_Q), skv = smem_u32(smem + C::OFF_KV);
+            bool ok = true;
+            uint32_t x0 = 0;                  // first K/V tile number of the piece
+            uint32_t pvs[2] = {0, 0};         // P V products issued
+            int np = 0;
+            // scores of Q tile q in buffer t; the weights in its columns have been used by then
+            auto scores = [&](int t, int q, uint32_t x) {
+                const uint32_t slot = x % NS;
+                ok = ok && mbar_wait(&kv_full[slot], (x / NS) & 1);
+                if (ok && pvs[t]) ok = mbar_wait(&pv_done[t], (pvs[t] - 1) & 1);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t d = tmem + t * CH_KEYS, qa = sq + q * C::TILE, ka = skv + slot * C::TILE;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * C::BOX + (ks & 3) * 32;
+                    tc_mma_bf16(d, umma_desc_k_sw128(qa + off), umma_desc_k_sw128(ka + off), C::IDESC_S, ks > 0 ? 1u : 0u);
+                }
+                tc_commit(&s_full[t]);
+                mbar_arrive(&s_full[t]);
+            };
+            auto values = [&](int t, bool acc, uint32_t x) {
+                const uint32_t slot = x % NS;
+                ok = ok && mbar_wait(&kv_full[slot], (x / NS) & 1);
+                if (ok) ok = mbar_wait(&p_full[t], pvs[t] & 1);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t va = skv + slot * C::TILE;
+#pragma unroll
+                for (int ks = 0; ks < CH_KEYS / 16; ++ks)
+                    tc_mma_bf16_ts(tmem + 256 + t * D, tmem + t * CH_KEYS + ks * 8,
+                                   umma_desc_mn_sw128(va + ks * 2048, C::BOX, 1024), C::IDESC_O, (acc || ks > 0) ? 1u : 0u);
+                tc_commit(&pv_done[t]);
+                ++pvs[t];
+            };
+            for (ChunkUnit u = u0; ok && u.b < p.B && u.U < hi; plan.next(u)) {
+                int tb, te;
+                if (!plan.piece(u, lo, hi, tb, te)) continue;
+                ok = mbar_wait(q_full, np & 1);
+                ++np;
+                if (!ok) break;
+                const int n = te - tb;
+                if (u.cost == 2) {
+                    const int n0 = min(te, u.tiles0) - tb;  // tiles of Q tile 0 (it may see none of these)
+                    if (n0 > 0) scores(0, 0, x0);
+                    scores(1, 1, x0);
+                    if (ok) tc_commit(&kv_empty[x0 % NS]);
+                    if (ok && n == 1) tc_commit(q_empty);
+                    // each Q tile's P V, then at once its next scores
+                    for (int k = 0; k < n && ok; ++k) {
+                        const uint32_t xv = x0 + 2 * k + 1, xk = xv + 1;
+                        if (k < n0) values(0, k > 0, xv);
+                        if (k + 1 < n0) scores(0, 0, xk);
+                        values(1, k > 0, xv);
+                        if (ok) tc_commit(&kv_empty[xv % NS]);
+                        if (k + 1 < n) {
+                            scores(1, 1, xk);
+                            if (ok) tc_commit(&kv_empty[xk % NS]);
+                            if (ok && k + 2 == n) tc_commit(q_empty);
+                        }
+                    }
+                } else {
+                    // one Q tile: even tiles in buffer 0, odd ones in buffer 1
+                    scores(0, 0, x0);
+                    if (ok) tc_commit(&kv_empty[x0 % NS]);
+                    if (n > 1) {
+                        scores(1, 0, x0 + 2);
+                        if (ok) tc_commit(&kv_empty[(x0 + 2) % NS]);
+                    }
+                    if (ok && n <= 2) tc_commit(q_empty);
+                    for (int k = 0; k < n && ok; ++k) {
+                        const int t = k & 1;
+                        values(t, k > 1, x0 + 2 * k + 1);
+                        if (ok) tc_commit(&kv_empty[(x0 + 2 * k + 1) % NS]);
+                        if (k + 2 < n) {
+                            scores(t, 0, x0 + 2 * k + 4);
+                            if (ok) tc_commit(&kv_empty[(x0 + 2 * k + 4) % NS]);
+                            if (ok && k + 3 == n) tc_commit(q_empty);
+                        }
+                    }
+                }
+                x0 += 2 * n;
+            }
+            if (!ok) {
+                *s_abort = 1;
+                report_status(p.dev_status, KVATTN_STATUS_TIMEOUT);
+            }
+            tc_commit(done);
+            mbar_wait(done, 0);
+        }
+    } else if (warp < 8) {
+        if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
+        // ===== softmax + epilogue: one thread per row, warps 0-3 buffer 0, warps 4-7 buffer 1 =====
+        const int t = warp >> 2, quarter = warp & 3;
+        const int r = quarter * 32 + lane;  // row of the Q tile = TMEM lane
+        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t s_addr = tmem + lane_off + t * CH_KEYS;
+        const uint32_t o_base = tmem + lane_off + 256;
+        const float sl2 = a.scale * kLog2e;
+        uint32_t it0 = 0;   // first tile number of the piece
+        uint32_t cnt = 0;   // tiles of this buffer so far
+        for (ChunkUnit u = u0; u.b < p.B && u.U < hi; plan.next(u)) {
+            int tb, te;
+            if (!plan.piece(u, lo, hi, tb, te)) continue;
+            const bool pair = u.cost == 2;  // two Q tiles; else one, its key tiles dealt out in turn
+            const int row = pair ? t * 128 + r : r;
+            const int tok0 = u.rb * w;
+            const int pos = u.s.base() + tok0 + (row >> gs);
+            const int pos_first = u.s.base() + tok0 + ((row - lane) >> gs);  // the warp's lowest
+            const bool active_warp = row - lane < u.rows;
+            const int n_my = pair ? max(min(te, t == 0 ? u.tiles0 : u.tiles) - tb, 0) : (te - tb + 1 - t) / 2;
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int k = 0; k < n_my; ++k, ++cnt) {
+                const int j = pair ? tb + k : tb + 2 * k + t;
+                const uint32_t it = it0 + (j - tb);
+                if (!warp_wait(&s_full[t], cnt & 1, s_abort)) continue;
+                tc_fence_after();
+                const int nv = min(u.keys - j * CH_KEYS, CH_KEYS);
+                if (!FP8 && nv < CH_KEYS) {
+                    // rows of V behind the last key in use were not loaded, or hold what nobody may see:
+                    // zeros, so that 0 * garbage cannot reach a sum (the P V waits for this warp)
+                    const uint32_t xv = 2 * it + 1;
+                    if (!warp_wait(&kv_full[xv % NS], (xv / NS) & 1, s_abort)) continue;
+                    if (r >= nv) {
+                        uint8_t* v = smem + C::OFF_KV + (xv % NS) * C::TILE + r * 128;
+#pragma unroll
+                        for (int i = 0; i < C::HALVES * 8; ++i)
+                            *reinterpret_cast<uint4*>(v + (i >> 3) * C::BOX + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                if (active_warp) {
+                    const uint32_t bad = s_bad[it % C::RING];
+                    const float* ks = s_sc + (it % C::RING) * 2 * CH_KEYS;
+                    const int lim = pos - j * CH_KEYS;  // keys 0 .. lim of the tile are seen
+                    const bool masked = pos_first - j * CH_KEYS < CH_KEYS - 1 || bad != 0;  // warp-uniform
+                    uint32_t sv[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, sv[c]);
+                    tmem_wait_ld();
+                    float mxc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_regs_ready(sv[c]);
+                        if constexpr (FP8) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                const float2 y = __fmul2_rn(make_float2(__uint_as_float(sv[c][i]), __uint_as_float(sv[c][i + 1])),
+                                                            *reinterpret_cast<const float2*>(ks + c * 32 + i));
+                                sv[c][i] = __float_as_uint(y.x);
+                                sv[c][i + 1] = __float_as_uint(y.y);
+                            }
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c * 32 + i > lim || (bad >> (c * 2 + i / 16) & 1u)) sv[c][i] = 0xff800000u;  // -inf
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            mxc[c] = fmax3(mxc[c], __uint_as_float(sv[c][i]), __uint_as_float(sv[c][i + 1]));
+                    }
+                    const float mx = fmaxf(fmaxf(mxc[0], mxc[1]), fmaxf(mxc[2], mxc[3])) * sl2;
+                    // the reference maximum moves (and O with it, for the warp together) only when the
+                    // row's maximum has grown by more than 2^8: the weights stay below 2^8
+                    const bool move = mx > m_run + kRescaleThreshold || m_run == -INFINITY;
+                    const float m_new = move ? fmaxf(mx, m_run) : m_run;
+                    const bool rescale = move && m_run != -INFINITY;
+                    if (__any_sync(0xffffffffu, rescale)) {
+                        const float alpha = rescale ? fast_exp2(m_run - m_new) : 1.f;
+                        l_run *= alpha;
+                        // (the scores of this tile were issued after the last P V had finished)
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t ov[32];
+                            tmem_ld32(o_base + t * D + c * 32, ov);
+                            tmem_wait_ld();
+                            tmem_regs_ready(ov);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                            tmem_st32(o_base + t * D + c * 32, ov);
+                        }
+                    }
+                    m_run = m_new;
+                    const float mu = m_run == -INFINITY ? 0.f : m_run;
+                    l_run += masked ? row_weights<FP8, true>(sv, sl2, mu, s_addr, ks + CH_KEYS)
+                                    : row_weights<FP8, false>(sv, sl2, mu, s_addr, ks + CH_KEYS);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[t]);
+            }
+            it0 += te - tb;
+            const bool ok = n_my == 0 || warp_wait(&pv_done[t], (cnt - 1) & 1, s_abort);
+            tc_fence_after();
+            // ---- the piece's rows: finished, or a partial for the merge ----
+            const int first = chunk_owner(u.U, N, G);
+            const int count = chunk_owner(u.U + static_cast<long long>(u.tiles - 1) * u.cost, N, G) - first + 1;
+            if (count > 1 && c == first && threadIdx.x == 0)
+                a.split_info[c] = make_int4(u.s.t0 + tok0, u.rows, u.kvh, count);
+            const long long tok = u.s.t0 + tok0 + (row >> gs);
+            const long long orow = tok * a.H + static_cast<long long>(u.kvh) * a.g + (row & (a.g - 1));
+            const long long prow = static_cast<long long>(c == first ? 2 * c + 1 : 2 * c) * CH_ROWS + row;
+            const bool use = ok && row < u.rows;
+            float m = m_run, l = l_run, w0 = 1.f, w1 = 0.f;  // weights of this buffer's (w0) and the other's sums
+            int c0 = 0, c1 = D / 32;
+            if (!pair) {
+                // join the two buffers: each group writes half of the columns
+                s_ml[t * 128 + r] = make_float2(m_run, l_run);
+                tc_fence_before();
+                named_bar_sync(1, 256);
+                tc_fence_after();
+                const float2 o = s_ml[(t ^ 1) * 128 + r];
+                m = fmaxf(m_run, o.x);
+                const float mu = m == -INFINITY ? 0.f : m;
+                w0 = m_run == -INFINITY ? 0.f : fast_exp2(m_run - mu);
+                w1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - mu);
+                l = w0 * l_run + w1 * o.y;
+                c0 = t * (D / 64);
+                c1 = c0 + D / 64;
+            } else if (m_run == -INFINITY) {
+                w0 = 0.f;  // nothing seen: the accumulator may never have been written
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            if (count == 1) {
+                w0 *= inv;
+                w1 *= inv;
+            }
+#pragma unroll 1
+            for (int cc = c0; cc < c1; ++cc) {
+                uint32_t ov[32];
+                tmem_ld32(o_base + t * D + cc * 32, ov);
+                tmem_wait_ld();
+                tmem_regs_ready(ov);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) ov[i] = w0 == 0.f ? 0u : __float_as_uint(__uint_as_float(ov[i]) * w0);
+                if (!pair) {
+                    uint32_t ow[32];
+                    tmem_ld32(o_base + (t ^ 1) * D + cc * 32, ow);
+                    tmem_wait_ld();
+                    tmem_regs_ready(ow);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (w1 != 0.f) ov[i] = __float_as_uint(fmaf(__uint_as_float(ow[i]), w1, __uint_as_float(ov[i])));
+                }
+                if (use && count == 1) {
+                    uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + cc * 32);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        dst[i / 8] = make_uint4(pack_bf16x2(__uint_as_float(ov[i]), __uint_as_float(ov[i + 1])),
+                                                pack_bf16x2(__uint_as_float(ov[i + 2]), __uint_as_float(ov[i + 3])),
+                                                pack_bf16x2(__uint_as_float(ov[i + 4]), __uint_as_float(ov[i + 5])),
+                                                pack_bf16x2(__uint_as_float(ov[i + 6]), __uint_as_float(ov[i + 7])));
+                } else if (use) {
+                    uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + cc * 32);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) dst[i / 4] = make_uint4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+                }
+            }
+            if (use && (pair || t == 0)) {
+                if (count == 1) {
+                    if (a.lse) a.lse[orow] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+                } else {
+                    a.part_ml[prow] = make_float2(m, l);
+                }
+            }
+            // the other group reads this buffer's accumulator: the next piece waits for it
+            tc_fence_before();
+            if (!pair) named_bar_sync(1, 256);
+        }
+    } else if (warp >= 12) {
+        if constexpr (FP8) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+            // ===== codes -> bf16 tiles in the 128-byte-swizzled layout =====
+            constexpr int CH = D / 16;  // 16-code chunks per row
+            const int tid = threadIdx.x - 384;
+            uint32_t x = 0;
+            bool ok = true;
+            for (ChunkUnit u = u0; ok && u.b < p.B && u.U < hi; plan.next(u)) {
+                int tb, te;
+                if (!plan.piece(u, lo, hi, tb, te)) continue;
+                for (int j = tb; j < te && ok; ++j) {
+                    const int nv = min(u.keys - j * CH_KEYS, CH_KEYS);
+                    const uint32_t it = x / 2;
+                    for (int kv = 0; kv < 2; ++kv, ++x) {
+                        const uint32_t ls = x % (LS > 0 ? LS : 1), slot = x % NS;
+                        ok = warp_wait(&land_full[ls], (x / (LS > 0 ? LS : 1)) & 1, s_abort);
+                        if (ok && x >= NS) ok = warp_wait(&kv_empty[slot], (x / NS - 1) & 1, s_abort);
+                        if (!ok) break;
+                        const uint32_t bad = s_bad[it % C::RING];
+                        const bool partial = nv < CH_KEYS || bad != 0;
+                        if (kv == 0 && partial && (tid >= nv || (bad >> (tid / 16) & 1u))) {
+                            float* sc = s_sc + (it % C::RING) * 2 * CH_KEYS + tid;
+                            sc[0] = 0.f;
+                            sc[CH_KEYS] = 0.f;
+                        }
+                        const uint8_t* src = smem + C::OFF_LAND + ls * C::CODES;
+                        uint8_t* dst = smem + C::OFF_KV + slot * C::TILE;
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) {
+                            const int id = i * 128 + tid, row = id / CH, ch = id % CH;
+                            const uint4 v = *reinterpret_cast<const uint4*>(src + id * 16);
+                            uint4 o0, o1;
+                            codes_to_bf16(v.x, o0.x, o0.y);
+                            codes_to_bf16(v.y, o0.z, o0.w);
+                            codes_to_bf16(v.z, o1.x, o1.y);
+                            codes_to_bf16(v.w, o1.z, o1.w);
+                            if (kv == 1 && partial && row >= nv) o0 = o1 = make_uint4(0, 0, 0, 0);
+                            uint8_t* d = dst + (ch >> 2) * C::BOX;
+                            // chunks of the upper half in the other order: their banks are the lower half's
+                            const int sw = ch >> 2, c0 = (ch & 3) * 2;
+                            *reinterpret_cast<uint4*>(d + swz128(row, c0 + sw)) = sw ? o1 : o0;
+                            *reinterpret_cast<uint4*>(d + swz128(row, c0 + (sw ^ 1))) = sw ? o0 : o1;
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&kv_full[slot]);
+                            mbar_arrive(&land_empty[ls]);
+                        }
+                    }
+                }
+            }
+        }
+    } else {
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");  // warp 11: idle
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---- merge of the split units ------------------------------------------------------
+// One warp per query row: with M = max m_i over the partials and w_i = 2^(m_i - M),
+// out = sum w_i O_i / sum w_i l_i and lse = ln 2 (M + log2 sum w_i l_i), in the
+// partials' order.
+constexpr int TM_WARPS = 8;
+
+template <int D>
+__global__ void __launch_bounds__(TM_WARPS * 32) chunk_tile_merge_kernel(ChunkArgs a)
+{
+    constexpr int PL = D / 32;
+    pdl_wait();
+    pdl_trigger();
+    const int f = blockIdx.x;
+    const int4 info = a.split_info[f];
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.y * TM_WARPS + (threadIdx.x >> 5);
+    if (row >= info.y || info.w < 2) return;
+    const int count = info.w;
+    float M = -INFINITY;
+    for (int i = lane; i < count; i += 32)
+        M = fmaxf(M, a.part_ml[static_cast<long long>(i == 0 ? 2 * f + 1 : 2 * (f + i)) * CH_ROWS + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float mu = M == -INFINITY ? 0.f : M;
+    float L = 0.f, acc[PL];
+#pragma unroll
+    for (int i = 0; i < PL; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+        const long long pr = static_cast<long long>(i == 0 ? 2 * f + 1 : 2 * (f + i)) * CH_ROWS + row;
+        const float2 ml = a.part_ml[pr];
+        const float wi = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mu);
+        L += wi * ml.y;
+        const float* o = a.part_o + pr * D + lane * PL;
+        if constexpr (PL == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(o);
+            acc[0] += wi * v.x;
+            acc[1] += wi * v.y;
+            acc[PL - 2] += wi * v.z;
+            acc[PL - 1] += wi * v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(o);
+            acc[0] += wi * v.x;
+            acc[1] += wi * v.y;
+        }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const long long orow = (static_cast<long long>(info.x) + row / a.g) * a.H + static_cast<long long>(info.z) * a.g + row % a.g;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * PL);
+#pragma unroll
+    for (int i = 0; i < PL; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+}
+
+template <int D, bool FP8>
+cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                         int num_sms, cudaStream_t stream)
+{
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(chunk_tile_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<D, FP8>::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) attr_set[dev] = true;
+    }
+    const int grid = num_sms < CHUNK_MAX_CTAS ? num_sms : CHUNK_MAX_CTAS;
+    e = launch_pdl(chunk_tile_kernel<D, FP8>, dim3(grid), dim3(TCfg<D, FP8>::THREADS), TCfg<D, FP8>::SMEM, stream, tm_q,
+                   tm_k, tm_v, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(chunk_tile_merge_kernel<D>, dim3(grid, CH_ROWS / TM_WARPS), dim3(TM_WARPS * 32), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_tile(const ChunkArgs& a, bool fp8, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                              const CUtensorMap& tm_v, int num_sms, cudaStream_t stream)
+{
+    if (a.d == 128)
+        return fp8 ? launch_typed<128, true>(a, tm_q, tm_k, tm_v, num_sms, stream)
+                   : launch_typed<128, false>(a, tm_q, tm_k, tm_v, num_sms, stream);
+    return fp8 ? launch_typed<64, true>(a, tm_q, tm_k, tm_v, num_sms, stream)
+               : launch_typed<64, false>(a, tm_q, tm_k, tm_v, num_sms, stream);
+}
+
+}  // namespace kvattn

@@ -63,7 +63,16 @@ struct ChunkArgs {
     float* lse;        // [n_tokens][H] or null
     int H, Hk, g, d, max_q;
     float scale;
+    // tensor-core kernel: split blocks, by the CTA that holds their first key tile (first token,
+    // rows, KV head, partials), and their partials: two slots of 256 rows per CTA
+    int4* split_info;
+    float2* part_ml;  // (maximum in log2 units, sum)
+    float* part_o;    // unnormalised
 };
+constexpr int CHUNK_MAX_CTAS = 148;
+constexpr int CHUNK_SLOT_ROWS = 256;
+cudaError_t launch_chunk_tile(const ChunkArgs& a, bool fp8, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                              const CUtensorMap& tm_v, int num_sms, cudaStream_t stream);
 cudaError_t launch_chunk(const ChunkArgs& a, bool fp8, int num_sms, cudaStream_t stream);
 
 // A sequence's share of the packed tokens and its length, forced into range.
@@ -72,7 +81,7 @@ struct PagedSeq {
     bool bad;  // something was out of range
 };
 
-__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& p, int c0, int c1, int len_raw)
+__host__ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& p, int c0, int c1, int len_raw)
 {
     PagedSeq s;
     s.t0 = min(max(c0, 0), p.n_tokens);
