@@ -50,6 +50,20 @@ __device__ __forceinline__ float2 exp2_poly2(float2 x)
                        __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
+// A stretch of one unit's key tiles, as warp 11 hands it to the others (rows = 0: no more).
+struct Piece {
+    int b, kvh;
+    int tok0;    // the block's first packed token
+    int pos0;    // its position
+    int rows, keys;
+    int tb, te;  // tiles
+    int tiles0;  // tiles that the first 128 rows see
+    int cost;    // 2: two Q tiles, 1: one
+    int count;   // pieces of the unit
+    int first;   // whether this is the first of them
+};
+constexpr int PIECES = 4;
+
 template <int D, bool FP8>
 struct TCfg {
     static constexpr int HALVES = D / 64;
@@ -68,9 +82,13 @@ struct TCfg {
     static constexpr int OFF_CU = OFF_U + (PAGED_MAX_B + 1) * 8;
     static constexpr int OFF_LEN = OFF_CU + (PAGED_MAX_B + 1) * 4;
     static constexpr int OFF_ML = (OFF_LEN + PAGED_MAX_B * 4 + 15) / 16 * 16;  // [2][128] (max, sum)
-    static constexpr int OFF_BAR = OFF_ML + 2 * 128 * 8;
-    // kv_full[NS], kv_empty[NS], land_full[LS], land_empty[LS], q_full, q_empty, s_full[2], p_full[2], pv_done[2], done
-    static constexpr int NBAR = 2 * NS + 2 * LS + 9;
+    static constexpr int OFF_PIECE = OFF_ML + 2 * 128 * 8;
+    static constexpr int OFF_BAR = OFF_PIECE + PIECES * static_cast<int>(sizeof(Piece));
+    // kv_full[NS], kv_empty[NS], land_full[LS], land_empty[LS], q_full, q_empty, s_full[2], p_full[2], pv_done[2],
+    // joined[2], piece_full[PIECES], piece_empty[PIECES], done
+    static constexpr int NBAR = 2 * NS + 2 * LS + 11 + 2 * PIECES;
+    // warps that take every piece: 8 of the softmax, MMA, K/V loads, Q loads, 4 of the widening
+    static constexpr int TAKERS = FP8 ? 15 : 11;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + RING * 4 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
@@ -100,6 +118,43 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
+// The MMA warp runs its loop with all lanes, so that the descriptors stay in uniform
+// registers (under a one-lane branch each operand of each MMA is moved there first, about
+// 100 cycles per instruction); only these instructions are for the elected lane.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t elect, uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(elect)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t elect, uint32_t d, uint32_t at, uint64_t bd, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(at), "l"(bd), "r"(idesc), "r"(acc), "r"(elect)
+        : "memory");
+}
+
+__device__ __forceinline__ void commit_to(uint32_t elect, uint64_t* bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(elect)
+        : "memory");
+}
+
 // One row's 128 scores (log2 units after sl2) -> weights to TMEM over the scores; returns their sum.
 // MASKED tiles take every exponential from the hardware unit, where 2^-inf is exactly 0;
 // otherwise a quarter go through the polynomial on the FMA pipe.
@@ -112,6 +167,11 @@ __device__ __forceinline__ float row_weights(const uint32_t (&sv)[4][32], float 
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         uint32_t pk[16];
+        float4 v4[FP8 ? 8 : 1];
+        if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v4[i] = reinterpret_cast<const float4*>(vs)[c * 8 + i];
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[c][2 * i]), __uint_as_float(sv[c][2 * i + 1])),
@@ -124,7 +184,7 @@ __device__ __forceinline__ float row_weights(const uint32_t (&sv)[4][32], float 
                 pr.y = fast_exp2(x.y);
             }
             acc[i & 3] = __fadd2_rn(acc[i & 3], pr);
-            if constexpr (FP8) pr = __fmul2_rn(pr, *reinterpret_cast<const float2*>(vs + c * 32 + 2 * i));
+            if constexpr (FP8) pr = __fmul2_rn(pr, (i & 1) ? make_float2(v4[i / 2].z, v4[i / 2].w) : make_float2(v4[i / 2].x, v4[i / 2].y));
             pk[i] = pack_bf16x2(pr.x, pr.y);
         }
         tmem_st16(s_addr + c * 16, pk);
@@ -151,7 +211,11 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
     uint64_t* s_full = q_full + 2;
     uint64_t* p_full = q_full + 4;
     uint64_t* pv_done = q_full + 6;
-    uint64_t* done = q_full + 8;
+    uint64_t* joined = q_full + 8;
+    uint64_t* piece_full = q_full + 10;
+    uint64_t* piece_empty = piece_full + PIECES;
+    uint64_t* done = piece_empty + PIECES;
+    const Piece* s_piece = reinterpret_cast<const Piece*>(smem + C::OFF_PIECE);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
     volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 16);  // [RING]: groups of 16 keys without a page
@@ -177,6 +241,11 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             mbar_init(&s_full[i], 2);  // the products' commit, and their issuer
             mbar_init(&p_full[i], 4);
             mbar_init(&pv_done[i], 1);
+            mbar_init(&joined[i], 8);
+        }
+        for (int i = 0; i < PIECES; ++i) {
+            mbar_init(&piece_full[i], 1);
+            mbar_init(&piece_empty[i], C::TAKERS);
         }
         mbar_init(done, 1);
         *s_abort = 0;
@@ -218,24 +287,26 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             if (a.lse && i % (D / 8) == 0) a.lse[row] = -INFINITY;
         }
     }
-    const long long N = plan.total();
-    // every CTA's stretch holds two points at least, so that it owns a tile of each unit it lies in
-    const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), N / 2 > 0 ? N / 2 : 1));
     const int c = blockIdx.x;
-    const bool active = N > 0 && c < G;
-    long long lo = 0, hi = 0;
-    ChunkUnit u0{};
-    u0.b = p.B;
-    if (active) {
-        lo = chunk_start(c, N, G);
-        hi = chunk_start(c + 1, N, G);
-        u0 = plan.find(lo);
-    }
-    // split units: told to the merge by the CTA of their first tile
-    if (threadIdx.x == 0) a.split_info[c] = make_int4(0, 0, 0, 0);
+    // piece i of this CTA, for a whole warp / for one thread; false: none left (or a wait ran out)
+    auto take = [&](int i, Piece& pc) {
+        const int k = i % PIECES;
+        if (!warp_wait(&piece_full[k], (i / PIECES) & 1, s_abort)) return false;
+        pc = s_piece[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&piece_empty[k]);
+        return pc.rows > 0;
+    };
+    auto take1 = [&](int i, Piece& pc) {
+        const int k = i % PIECES;
+        if (*s_abort || !mbar_wait(&piece_full[k], (i / PIECES) & 1)) return false;
+        pc = s_piece[k];
+        mbar_arrive(&piece_empty[k]);
+        return pc.rows > 0;
+    };
 
     if (warp == 9) {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
         // ===== K/V pages: lane i takes box i of a tile (page, and for bf16 its 64-column half) =====
         const int bp_shift = min(p.page_shift, 7);  // rows of a box: a page's, 128 at most
@@ -246,9 +317,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         uint32_t x = 0;  // K and V tiles so far
         uint32_t it = 0;
         bool ok = true;
-        for (ChunkUnit u = u0; ok && u.b < p.B && u.U < hi; plan.next(u)) {
-            int tb, te;
-            if (!plan.piece(u, lo, hi, tb, te)) continue;
+        Piece u;
+        for (int n = 0; ok && take(n, u); ++n) {
+            const int tb = u.tb, te = u.te;
             const int32_t* pt = p.page_table + static_cast<long long>(u.b) * p.max_pages;
             auto entry = [&](int j) {
                 const int row = j * CH_KEYS + (box << bp_shift);
@@ -313,14 +384,13 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             for (uint32_t i = x > R ? x - R : 0; i < x; ++i) mbar_wait(&full[i % R], (i / R) & 1);
         }
     } else if (warp == 10) {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
         // ===== Q: [128 / g tokens][g heads] boxes, one or two tiles a piece =====
         if (lane == 0) {
             int np = 0;
-            for (ChunkUnit u = u0; u.b < p.B && u.U < hi; plan.next(u)) {
-                int tb, te;
-                if (!plan.piece(u, lo, hi, tb, te)) continue;
+            Piece u;
+            while (take1(np, u)) {
                 if (np > 0 && (*s_abort || !mbar_wait(q_empty, (np - 1) & 1))) {
                     *s_abort = 1;
                     break;
@@ -330,55 +400,58 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
 #pragma unroll
                     for (int h = 0; h < C::HALVES; ++h)
                         tma_load_3d(smem + C::OFF_Q + t * C::TILE + h * C::BOX, &tm_q, q_full, h * 64, u.kvh * a.g,
-                                    u.s.t0 + u.rb * w + t * (w / 2));
+                                    u.tok0 + t * (w / 2));
                 ++np;
             }
             if (np > 0) mbar_wait(q_full, (np - 1) & 1);
         }
     } else if (warp == 8) {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
-        // ===== MMA issue (one thread) =====
-        if (lane == 0) {
+        // ===== MMA issue =====
+        {
+            const uint32_t el = elect_one();
             const uint32_t sq = smem_u32(smem + C::OFF_Q), skv = smem_u32(smem + C::OFF_KV);
             bool ok = true;
             uint32_t x0 = 0;                  // first K/V tile number of the piece
-            uint32_t pvs[2] = {0, 0};         // P V products issued
+            uint32_t pv0 = 0, pv1 = 0;        // P V products issued to each buffer
             int np = 0;
             // scores of Q tile q in buffer t; the weights in its columns have been used by then
             auto scores = [&](int t, int q, uint32_t x) {
                 const uint32_t slot = x % NS;
-                ok = ok && mbar_wait(&kv_full[slot], (x / NS) & 1);
-                if (ok && pvs[t]) ok = mbar_wait(&pv_done[t], (pvs[t] - 1) & 1);
+                ok = ok && warp_wait(&kv_full[slot], (x / NS) & 1, s_abort);
+                const uint32_t pv = t ? pv1 : pv0;
+                if (ok && pv) ok = warp_wait(&pv_done[t], (pv - 1) & 1, s_abort);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t d = tmem + t * CH_KEYS, qa = sq + q * C::TILE, ka = skv + slot * C::TILE;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t off = (ks >> 2) * C::BOX + (ks & 3) * 32;
-                    tc_mma_bf16(d, umma_desc_k_sw128(qa + off), umma_desc_k_sw128(ka + off), C::IDESC_S, ks > 0 ? 1u : 0u);
+                    mma_ss(el, d, umma_desc_k_sw128(qa + off), umma_desc_k_sw128(ka + off), C::IDESC_S, ks > 0 ? 1u : 0u);
                 }
-                tc_commit(&s_full[t]);
-                mbar_arrive(&s_full[t]);
+                commit_to(el, &s_full[t]);
+                if (el) mbar_arrive(&s_full[t]);
             };
             auto values = [&](int t, bool acc, uint32_t x) {
                 const uint32_t slot = x % NS;
-                ok = ok && mbar_wait(&kv_full[slot], (x / NS) & 1);
-                if (ok) ok = mbar_wait(&p_full[t], pvs[t] & 1);
+                ok = ok && warp_wait(&kv_full[slot], (x / NS) & 1, s_abort);
+                if (ok) ok = warp_wait(&p_full[t], (t ? pv1 : pv0) & 1, s_abort);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t va = skv + slot * C::TILE;
 #pragma unroll
                 for (int ks = 0; ks < CH_KEYS / 16; ++ks)
-                    tc_mma_bf16_ts(tmem + 256 + t * D, tmem + t * CH_KEYS + ks * 8,
+                    mma_ts(el, tmem + 256 + t * D, tmem + t * CH_KEYS + ks * 8,
                                    umma_desc_mn_sw128(va + ks * 2048, C::BOX, 1024), C::IDESC_O, (acc || ks > 0) ? 1u : 0u);
-                tc_commit(&pv_done[t]);
-                ++pvs[t];
+                commit_to(el, &pv_done[t]);
+                if (t) ++pv1;
+                else ++pv0;
             };
-            for (ChunkUnit u = u0; ok && u.b < p.B && u.U < hi; plan.next(u)) {
-                int tb, te;
-                if (!plan.piece(u, lo, hi, tb, te)) continue;
-                ok = mbar_wait(q_full, np & 1);
+            Piece u;
+            while (ok && take(np, u)) {
+                const int tb = u.tb, te = u.te;
+                ok = warp_wait(q_full, np & 1, s_abort);
                 ++np;
                 if (!ok) break;
                 const int n = te - tb;
@@ -386,49 +459,47 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     const int n0 = min(te, u.tiles0) - tb;  // tiles of Q tile 0 (it may see none of these)
                     if (n0 > 0) scores(0, 0, x0);
                     scores(1, 1, x0);
-                    if (ok) tc_commit(&kv_empty[x0 % NS]);
-                    if (ok && n == 1) tc_commit(q_empty);
+                    if (ok) commit_to(el, &kv_empty[x0 % NS]);
+                    if (ok && n == 1) commit_to(el, q_empty);
                     // each Q tile's P V, then at once its next scores
                     for (int k = 0; k < n && ok; ++k) {
                         const uint32_t xv = x0 + 2 * k + 1, xk = xv + 1;
                         if (k < n0) values(0, k > 0, xv);
                         if (k + 1 < n0) scores(0, 0, xk);
                         values(1, k > 0, xv);
-                        if (ok) tc_commit(&kv_empty[xv % NS]);
+                        if (ok) commit_to(el, &kv_empty[xv % NS]);
                         if (k + 1 < n) {
                             scores(1, 1, xk);
-                            if (ok) tc_commit(&kv_empty[xk % NS]);
-                            if (ok && k + 2 == n) tc_commit(q_empty);
+                            if (ok) commit_to(el, &kv_empty[xk % NS]);
+                            if (ok && k + 2 == n) commit_to(el, q_empty);
                         }
                     }
                 } else {
                     // one Q tile: even tiles in buffer 0, odd ones in buffer 1
                     scores(0, 0, x0);
-                    if (ok) tc_commit(&kv_empty[x0 % NS]);
+                    if (ok) commit_to(el, &kv_empty[x0 % NS]);
                     if (n > 1) {
                         scores(1, 0, x0 + 2);
-                        if (ok) tc_commit(&kv_empty[(x0 + 2) % NS]);
+                        if (ok) commit_to(el, &kv_empty[(x0 + 2) % NS]);
                     }
-                    if (ok && n <= 2) tc_commit(q_empty);
+                    if (ok && n <= 2) commit_to(el, q_empty);
                     for (int k = 0; k < n && ok; ++k) {
                         const int t = k & 1;
                         values(t, k > 1, x0 + 2 * k + 1);
-                        if (ok) tc_commit(&kv_empty[(x0 + 2 * k + 1) % NS]);
+                        if (ok) commit_to(el, &kv_empty[(x0 + 2 * k + 1) % NS]);
                         if (k + 2 < n) {
                             scores(t, 0, x0 + 2 * k + 4);
-                            if (ok) tc_commit(&kv_empty[(x0 + 2 * k + 4) % NS]);
-                            if (ok && k + 3 == n) tc_commit(q_empty);
+                            if (ok) commit_to(el, &kv_empty[(x0 + 2 * k + 4) % NS]);
+                            if (ok && k + 3 == n) commit_to(el, q_empty);
                         }
                     }
                 }
                 x0 += 2 * n;
             }
-            if (!ok) {
-                *s_abort = 1;
-                report_status(p.dev_status, KVATTN_STATUS_TIMEOUT);
-            }
-            tc_commit(done);
+            if (*s_abort && el) report_status(p.dev_status, KVATTN_STATUS_TIMEOUT);
+            commit_to(el, done);
             mbar_wait(done, 0);
+            __syncwarp();
         }
     } else if (warp < 8) {
         if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
@@ -442,16 +513,16 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         const float sl2 = a.scale * kLog2e;
         uint32_t it0 = 0;   // first tile number of the piece
         uint32_t cnt = 0;   // tiles of this buffer so far
-        for (ChunkUnit u = u0; u.b < p.B && u.U < hi; plan.next(u)) {
-            int tb, te;
-            if (!plan.piece(u, lo, hi, tb, te)) continue;
+        uint32_t joins = 0;
+        Piece u;
+        for (int n = 0; take(n, u); ++n) {
+            const int tb = u.tb, te = u.te;
             const bool pair = u.cost == 2;  // two Q tiles; else one, its key tiles dealt out in turn
             const int row = pair ? t * 128 + r : r;
-            const int tok0 = u.rb * w;
-            const int pos = u.s.base() + tok0 + (row >> gs);
-            const int pos_first = u.s.base() + tok0 + ((row - lane) >> gs);  // the warp's lowest
+            const int pos = u.pos0 + (row >> gs);
+            const int pos_first = u.pos0 + ((row - lane) >> gs);  // the warp's lowest
             const bool active_warp = row - lane < u.rows;
-            const int n_my = pair ? max(min(te, t == 0 ? u.tiles0 : u.tiles) - tb, 0) : (te - tb + 1 - t) / 2;
+            const int n_my = pair ? max((t == 0 ? min(te, u.tiles0) : te) - tb, 0) : (te - tb + 1 - t) / 2;
             float m_run = -INFINITY, l_run = 0.f;
             for (int k = 0; k < n_my; ++k, ++cnt) {
                 const int j = pair ? tb + k : tb + 2 * k + t;
@@ -487,11 +558,16 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                         tmem_regs_ready(sv[c]);
                         if constexpr (FP8) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const float2 y = __fmul2_rn(make_float2(__uint_as_float(sv[c][i]), __uint_as_float(sv[c][i + 1])),
-                                                            *reinterpret_cast<const float2*>(ks + c * 32 + i));
-                                sv[c][i] = __float_as_uint(y.x);
-                                sv[c][i + 1] = __float_as_uint(y.y);
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 k4 = *reinterpret_cast<const float4*>(ks + c * 32 + i);
+                                const float2 y0 = __fmul2_rn(make_float2(__uint_as_float(sv[c][i]), __uint_as_float(sv[c][i + 1])),
+                                                             make_float2(k4.x, k4.y));
+                                const float2 y1 = __fmul2_rn(make_float2(__uint_as_float(sv[c][i + 2]), __uint_as_float(sv[c][i + 3])),
+                                                             make_float2(k4.z, k4.w));
+                                sv[c][i] = __float_as_uint(y0.x);
+                                sv[c][i + 1] = __float_as_uint(y0.y);
+                                sv[c][i + 2] = __float_as_uint(y1.x);
+                                sv[c][i + 3] = __float_as_uint(y1.y);
                             }
                         }
                         if (masked) {
@@ -538,13 +614,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             const bool ok = n_my == 0 || warp_wait(&pv_done[t], (cnt - 1) & 1, s_abort);
             tc_fence_after();
             // ---- the piece's rows: finished, or a partial for the merge ----
-            const int first = chunk_owner(u.U, N, G);
-            const int count = chunk_owner(u.U + static_cast<long long>(u.tiles - 1) * u.cost, N, G) - first + 1;
-            if (count > 1 && c == first && threadIdx.x == 0)
-                a.split_info[c] = make_int4(u.s.t0 + tok0, u.rows, u.kvh, count);
-            const long long tok = u.s.t0 + tok0 + (row >> gs);
-            const long long orow = tok * a.H + static_cast<long long>(u.kvh) * a.g + (row & (a.g - 1));
-            const long long prow = static_cast<long long>(c == first ? 2 * c + 1 : 2 * c) * CH_ROWS + row;
+            const long long orow = (static_cast<long long>(u.tok0) + (row >> gs)) * a.H +
+                                   static_cast<long long>(u.kvh) * a.g + (row & (a.g - 1));
+            const long long prow = static_cast<long long>(2 * c + u.first) * CH_ROWS + row;
             const bool use = ok && row < u.rows;
             float m = m_run, l = l_run, w0 = 1.f, w1 = 0.f;  // weights of this buffer's (w0) and the other's sums
             int c0 = 0, c1 = D / 32;
@@ -552,7 +624,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 // join the two buffers: each group writes half of the columns
                 s_ml[t * 128 + r] = make_float2(m_run, l_run);
                 tc_fence_before();
-                named_bar_sync(1, 256);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&joined[0]);
+                warp_wait(&joined[0], joins & 1, s_abort);
                 tc_fence_after();
                 const float2 o = s_ml[(t ^ 1) * 128 + r];
                 m = fmaxf(m_run, o.x);
@@ -566,7 +640,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 w0 = 0.f;  // nothing seen: the accumulator may never have been written
             }
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            if (count == 1) {
+            if (u.count == 1) {
                 w0 *= inv;
                 w1 *= inv;
             }
@@ -587,7 +661,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     for (int i = 0; i < 32; ++i)
                         if (w1 != 0.f) ov[i] = __float_as_uint(fmaf(__uint_as_float(ow[i]), w1, __uint_as_float(ov[i])));
                 }
-                if (use && count == 1) {
+                if (use && u.count == 1) {
                     uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + cc * 32);
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
@@ -602,7 +676,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 }
             }
             if (use && (pair || t == 0)) {
-                if (count == 1) {
+                if (u.count == 1) {
                     if (a.lse) a.lse[orow] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
                 } else {
                     a.part_ml[prow] = make_float2(m, l);
@@ -610,20 +684,24 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             }
             // the other group reads this buffer's accumulator: the next piece waits for it
             tc_fence_before();
-            if (!pair) named_bar_sync(1, 256);
+            if (!pair) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&joined[1]);
+                warp_wait(&joined[1], joins & 1, s_abort);
+                ++joins;
+            }
         }
     } else if (warp >= 12) {
         if constexpr (FP8) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
             // ===== codes -> bf16 tiles in the 128-byte-swizzled layout =====
             constexpr int CH = D / 16;  // 16-code chunks per row
             const int tid = threadIdx.x - 384;
             uint32_t x = 0;
             bool ok = true;
-            for (ChunkUnit u = u0; ok && u.b < p.B && u.U < hi; plan.next(u)) {
-                int tb, te;
-                if (!plan.piece(u, lo, hi, tb, te)) continue;
-                for (int j = tb; j < te && ok; ++j) {
+            Piece u;
+            for (int n = 0; ok && take(n, u); ++n) {
+                for (int j = u.tb; j < u.te && ok; ++j) {
                     const int nv = min(u.keys - j * CH_KEYS, CH_KEYS);
                     const uint32_t it = x / 2;
                     for (int kv = 0; kv < 2; ++kv, ++x) {
@@ -640,7 +718,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                         }
                         const uint8_t* src = smem + C::OFF_LAND + ls * C::CODES;
                         uint8_t* dst = smem + C::OFF_KV + slot * C::TILE;
-#pragma unroll
+#pragma unroll 2
                         for (int i = 0; i < CH; ++i) {
                             const int id = i * 128 + tid, row = id / CH, ch = id % CH;
                             const uint4 v = *reinterpret_cast<const uint4*>(src + id * 16);
@@ -667,8 +745,51 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             }
         }
     } else {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");  // warp 11: idle
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+        // ===== warp 11: this CTA's pieces =====
+        if (lane == 0) {
+            const long long N = plan.total();
+            // every CTA's stretch holds two points at least, so that it owns a tile of each unit it lies in
+            const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), N / 2 > 0 ? N / 2 : 1));
+            int4 split = make_int4(0, 0, 0, 0);
+            int np = 0;
+            bool ok = true;
+            auto put = [&](const Piece& pc) {
+                const int k = np % PIECES;
+                if (np >= PIECES && !(ok = !*s_abort && mbar_wait(&piece_empty[k], (np / PIECES - 1) & 1))) {
+                    *s_abort = 1;
+                    return;
+                }
+                *reinterpret_cast<Piece*>(smem + C::OFF_PIECE + k * sizeof(Piece)) = pc;
+                mbar_arrive(&piece_full[k]);
+                ++np;
+            };
+            if (N > 0 && c < G) {
+                const long long lo = chunk_start(c, N, G), hi = chunk_start(c + 1, N, G);
+                for (ChunkUnit u = plan.find(lo); ok && u.b < p.B && u.U < hi; plan.next(u)) {
+                    Piece pc;
+                    if (!plan.piece(u, lo, hi, pc.tb, pc.te)) continue;
+                    const int f = chunk_owner(u.U, N, G);
+                    pc.b = u.b;
+                    pc.kvh = u.kvh;
+                    pc.tok0 = u.s.t0 + u.rb * w;
+                    pc.pos0 = u.s.base() + u.rb * w;
+                    pc.rows = u.rows;
+                    pc.keys = u.keys;
+                    pc.tiles0 = u.tiles0;
+                    pc.cost = u.cost;
+                    pc.count = chunk_owner(u.U + static_cast<long long>(u.tiles - 1) * u.cost, N, G) - f + 1;
+                    pc.first = f == c;
+                    if (pc.count > 1 && pc.first) split = make_int4(pc.tok0, pc.rows, pc.kvh, pc.count);
+                    put(pc);
+                }
+            }
+            // the merge finds a split unit at the CTA of its first tile
+            a.split_info[c] = split;
+            Piece none{};
+            if (ok) put(none);
+        }
     }
     tc_fence_before();
     __syncthreads();
