@@ -104,18 +104,21 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// Map of [z][y][x] with byte strides: bf16 in 128-byte-swizzled boxes 64 wide, or bytes in plain
-// boxes of the whole width; out-of-range parts of a box read as zero.
-int encode_map(const char* name, CUtensorMap* map, const void* base, bool bytes, uint64_t x, uint64_t y, uint64_t z,
-               uint64_t y_stride, uint64_t z_stride, uint32_t box_y, uint32_t box_z)
+// Map of [z][y][x] with byte strides, boxes 128 bytes wide (64 bf16, 128-byte swizzle) or, over
+// bytes, `box_x` wide (64: 64-byte swizzle, else none); what lies outside reads as zero.
+int encode_map(const char* name, CUtensorMap* map, const void* base, uint32_t byte_box_x, uint64_t x, uint64_t y,
+               uint64_t z, uint64_t y_stride, uint64_t z_stride, uint32_t box_y, uint32_t box_z, bool swizzle64 = false)
 {
     auto fn = encode_fn();
     if (!fn) return record_error(KVATTN_ERR_CUDA, "%s: cuTensorMapEncodeTiled is unavailable", name);
+    const bool bytes = byte_box_x > 0;
     const cuuint64_t dims[3] = {x, y, z}, strides[2] = {y_stride, z_stride};
-    const cuuint32_t box[3] = {bytes ? static_cast<cuuint32_t>(x) : 64u, box_y, box_z}, one[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {bytes ? byte_box_x : 64u, box_y, box_z}, one[3] = {1, 1, 1};
     const CUresult r = fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                           const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                          !bytes      ? CU_TENSOR_MAP_SWIZZLE_128B
+                          : swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                      : CU_TENSOR_MAP_SWIZZLE_NONE,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return record_error(KVATTN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", name, static_cast<int>(r));
@@ -124,13 +127,18 @@ int encode_map(const char* name, CUtensorMap* map, const void* base, bool bytes,
 
 constexpr size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
-// The chunk workspace: the decode kernels' zero region, then the split blocks' records and partials.
+// Whether a call's (sequence, KV head)s have 16 query rows at most (the row kernel's), by what the host knows.
+bool few_rows(int n_tokens, int max_q, int g) { return static_cast<long long>(max_q <= 0 || max_q > n_tokens ? n_tokens : max_q) * g <= kvattn::CHUNK_FEW_ROWS; }
+
+// The chunk workspace: the zero region (counters), then the partials.
 struct ChunkWorkspace {
-    size_t info = KVATTN_DECODE_WS_ZERO_BYTES, ml, o, total;
-    explicit ChunkWorkspace(int d)
+    size_t info = KVATTN_DECODE_WS_ZERO_BYTES, join, ml, o, total;
+    ChunkWorkspace(bool few, int d)
     {
-        const size_t rows = size_t(2) * kvattn::CHUNK_MAX_CTAS * kvattn::CHUNK_SLOT_ROWS;
-        ml = align_up(info + kvattn::CHUNK_MAX_CTAS * sizeof(int4));
+        const size_t rows = few ? size_t(2) * kvattn::CHUNK_MAX_SLOTS * kvattn::CHUNK_FEW_ROWS
+                                : size_t(2) * kvattn::CHUNK_MAX_CTAS * kvattn::CHUNK_SLOT_ROWS;
+        join = align_up(info + kvattn::CHUNK_MAX_CTAS * sizeof(int4));
+        ml = align_up(join + (few ? rows * sizeof(float2) : 0));
         o = align_up(ml + rows * sizeof(float2));
         total = o + rows * d * sizeof(float);
     }
@@ -216,17 +224,23 @@ int chunk(const char* name, bool fp8, const kvattn_bf16* q, int64_t q_stride, co
     a.d = head_dim;
     a.max_q = max_q <= 0 || max_q > n_tokens ? n_tokens : max_q;
     a.scale = scale;
-    const ChunkWorkspace ws(head_dim);
+    const bool few = few_rows(n_tokens, max_q, g);
+    const ChunkWorkspace ws(few, head_dim);
     uint8_t* wp = static_cast<uint8_t*>(workspace);
+    a.counters = reinterpret_cast<int*>(wp);
     a.split_info = reinterpret_cast<int4*>(wp + ws.info);
+    a.join_ml = reinterpret_cast<float2*>(wp + ws.join);
     a.part_ml = reinterpret_cast<float2*>(wp + ws.ml);
     a.part_o = reinterpret_cast<float*>(wp + ws.o);
-    const uint64_t es = fp8 ? 1 : 2, row = head_dim * es, planes = static_cast<uint64_t>(n_pages) * n_kv_head;
-    const uint32_t box = page_size < 128 ? page_size : 128;
+    const uint64_t row = head_dim * (fp8 ? 1 : 2), planes = static_cast<uint64_t>(n_pages) * n_kv_head;
+    const uint32_t tile = few ? 64 : 128, box = page_size < static_cast<int>(tile) ? page_size : tile;
+    const uint32_t byte_box = fp8 ? (few ? 64 : head_dim) : 0;
     CUtensorMap mq, mk, mv;
-    if ((rc = encode_map(name, &mq, q, false, head_dim, n_head, n_tokens, head_dim * 2, q_stride * 2, g, 128 / g)) != KVATTN_OK ||
-        (rc = encode_map(name, &mk, k_pages, fp8, head_dim, page_size, planes, row, row * page_size, box, 1)) != KVATTN_OK ||
-        (rc = encode_map(name, &mv, v_pages, fp8, head_dim, page_size, planes, row, row * page_size, box, 1)) != KVATTN_OK)
+    if ((rc = encode_map(name, &mk, k_pages, byte_box, head_dim, page_size, planes, row, row * page_size, box, 1, few)) != KVATTN_OK ||
+        (rc = encode_map(name, &mv, v_pages, byte_box, head_dim, page_size, planes, row, row * page_size, box, 1, few)) != KVATTN_OK)
+        return rc;
+    if (few) return finish(kvattn::launch_chunk_rows(a, fp8, mk, mv, sms, static_cast<cudaStream_t>(stream)), name);
+    if ((rc = encode_map(name, &mq, q, 0, head_dim, n_head, n_tokens, head_dim * 2, q_stride * 2, g, 128 / g)) != KVATTN_OK)
         return rc;
     return finish(kvattn::launch_chunk_tile(a, fp8, mq, mk, mv, sms, static_cast<cudaStream_t>(stream)), name);
 }
@@ -288,10 +302,8 @@ int kv_read_paged_fp8(const uint8_t* k_codes, const float* k_scales, const uint8
 
 size_t attn_chunk_paged_workspace_bytes(int B, int n_tokens, int max_q, int n_head, int n_kv_head, int head_dim)
 {
-    (void)n_tokens;
-    (void)max_q;
     if (B < 1 || n_head < 1 || n_kv_head < 1 || n_head % n_kv_head || head_dim < 1) return 0;
-    return ChunkWorkspace(head_dim).total;
+    return ChunkWorkspace(few_rows(n_tokens, max_q, n_head / n_kv_head), head_dim).total;
 }
 
 int attn_chunk_paged(const kvattn_bf16* q, int64_t q_stride, const int32_t* cu, const int32_t* seq_lens,

@@ -63,17 +63,22 @@ struct ChunkArgs {
     float* lse;        // [n_tokens][H] or null
     int H, Hk, g, d, max_q;
     float scale;
-    // tensor-core kernel: split blocks, by the CTA that holds their first key tile (first token,
-    // rows, KV head, partials), and their partials: two slots of 256 rows per CTA
-    int4* split_info;
+    // partials of units that several CTAs share: two slots of rows per CTA
     float2* part_ml;  // (maximum in log2 units, sum)
     float* part_o;    // unnormalised
+    int4* split_info;  // tile kernel: split blocks, by the CTA of their first key tile (first token, rows, KV head, pieces)
+    float2* join_ml;   // row kernel: (maximum, sum) of joined groups of partials
+    int* counters;     // row kernel: pieces that have finished (zero between calls)
 };
-constexpr int CHUNK_MAX_CTAS = 148;
+constexpr int CHUNK_MAX_CTAS = 148;     // tile kernel: at most this many CTAs, with slots of 256 rows
 constexpr int CHUNK_SLOT_ROWS = 256;
+constexpr int CHUNK_FEW_ROWS = 16;      // row kernel: query rows of a (sequence, KV head), and of a slot
+constexpr int CHUNK_MAX_SLOTS = 296;    // row kernel: at most this many CTAs
+static_assert(3 * CHUNK_MAX_SLOTS * 4 <= KVATTN_DECODE_WS_ZERO_BYTES, "counters");
+cudaError_t launch_chunk_rows(const ChunkArgs& a, bool fp8, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
+                              cudaStream_t stream);
 cudaError_t launch_chunk_tile(const ChunkArgs& a, bool fp8, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                               const CUtensorMap& tm_v, int num_sms, cudaStream_t stream);
-cudaError_t launch_chunk(const ChunkArgs& a, bool fp8, int num_sms, cudaStream_t stream);
 
 // A sequence's share of the packed tokens and its length, forced into range.
 struct PagedSeq {
