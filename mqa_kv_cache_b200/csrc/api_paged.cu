@@ -127,7 +127,7 @@ int encode_map(const char* name, CUtensorMap* map, const void* base, uint32_t by
 
 constexpr size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Whether a call's (sequence, KV head)s have 16 query rows at most (the row kernel's), by what the host knows.
+// Whether a call's (sequence, KV head)s have few query rows (the row kernel's), by what the host knows.
 bool few_rows(int n_tokens, int max_q, int g) { return static_cast<long long>(max_q <= 0 || max_q > n_tokens ? n_tokens : max_q) * g <= kvattn::CHUNK_FEW_ROWS; }
 
 // The chunk workspace: the zero region (counters), then the partials.

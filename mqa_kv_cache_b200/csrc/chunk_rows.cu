@@ -3,9 +3,9 @@
 //
 // Method: out = softmax_{j <= p} (scale q . k_j) v_j for the query at position p, query
 // head h reading KV head h / g ("注意力变体与 MoE", GQA attention(): the g heads of a
-// group share one K/V); all rows of a (sequence, KV head), its tokens times g heads, 16
-// at most, are the M rows of one mma.sync tile, so every cached row is read once.  The
-// cache streams from HBM at 4 * 16 FLOP a byte or less: the kernel is bound by that read.
+// group share one K/V); all rows of a (sequence, KV head), its tokens times g heads, 32
+// at most, are the M rows of one or two mma.sync tiles, so every cached row is read once
+// and the kernel is bound by that read.
 //
 // Work: the 64-key tiles of all (sequence, KV head) units form one line, dealt out to the
 // CTAs in equal stretches (as decode_plan.cuh does for contiguous caches); a stretch of a
@@ -13,9 +13,10 @@
 // an unnormalised partial and the CTA that finishes last joins them, in groups of 16
 // pieces and then the groups, always in the same order.
 //
-// Warps 0-3: 16 keys of every tile each, with their own running maximum and sum, joined
-// at the end of a piece.  Warp 4: loads (one box per page and 64-column half, page
-// entries fetched one tile ahead; the piece's query rows).  Warp 5: the pieces.
+// Four warps per 16 query rows: 16 keys of every tile each, with their own running maximum
+// and sum, joined at the end of a piece.  One warp loads (one box per page and 64-column
+// half, page entries fetched one tile ahead; the piece's query rows), the last one makes
+// the pieces.
 //
 // FP8: the codes become fp16 in registers, one conversion for two of them (exact).  K: a
 // thread's 16 codes of a key are one load, the k order of the MMA being free as long as Q
@@ -33,9 +34,6 @@ namespace kvattn {
 namespace {
 
 constexpr int RK = 64;        // keys per tile
-constexpr int RM = 16;        // query rows
-constexpr int RW = 4;         // consumer warps
-constexpr int RTHREADS = 32 * (RW + 2);
 constexpr int RGROUP = 16;    // pieces joined together
 constexpr int RPIECES = 4;    // pieces handed out ahead
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -50,23 +48,27 @@ struct RowPiece {
     int count;      // pieces of the unit
 };
 
-template <int D, bool FP8>
+// NMT: 16-row tiles of query rows; each has four consumer warps
+template <int D, bool FP8, int NMT>
 struct RCfg {
-    static constexpr int CTAS = FP8 ? 2 : 1;  // per SM
+    static constexpr int RM = 16 * NMT;
+    static constexpr int RW = 4 * NMT;
+    static constexpr int THREADS = 32 * (RW + 2);
+    static constexpr int CTAS = FP8 && NMT == 1 ? 2 : 1;  // per SM
     static constexpr int HALVES = D / 64;
     static constexpr int ROWB = FP8 ? 64 : 128;       // bytes of a 64-column row in shared memory
     static constexpr int BOX = RK * ROWB;
     static constexpr int TILE = HALVES * BOX;          // K or V
     static constexpr int SCB = FP8 ? 2 * RK * 4 : 0;   // their scales
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int STAGES = (FP8 ? 4 : 5) * (D == 128 ? 1 : 2);
+    static constexpr int STAGES = (FP8 ? (NMT == 1 ? 4 : 8) : 5) * (D == 128 ? 1 : 2);
     static constexpr int SCR = D + 8;                  // floats per scratch row
     static constexpr int OFF_SC = STAGES * STAGE;
     static constexpr int OFF_Q = OFF_SC + STAGES * SCB;  // two pieces' query rows
     static constexpr int QB = RM * D * 2;
-    static constexpr int OFF_O = OFF_Q + 2 * QB;         // [2][16][SCR]
-    static constexpr int OFF_ML = OFF_O + 2 * RM * SCR * 4;  // [4][16] (m, l)
-    static constexpr int OFF_U = OFF_ML + RW * RM * 8;
+    static constexpr int OFF_O = OFF_Q + 2 * QB;         // [NMT][2][16][SCR]
+    static constexpr int OFF_ML = OFF_O + 2 * RM * SCR * 4;  // [RW][16] (m, l)
+    static constexpr int OFF_U = OFF_ML + RW * 16 * 8;
     static constexpr int OFF_PIECE = OFF_U + (PAGED_MAX_B + 1) * 8;
     static constexpr int OFF_BAR = OFF_PIECE + (RPIECES * static_cast<int>(sizeof(RowPiece)) + 7) / 8 * 8;
     // full[STAGES], empty[STAGES], q_full[2], q_empty[2], piece_full[RPIECES], piece_empty[RPIECES]
@@ -111,7 +113,7 @@ __device__ __forceinline__ uint32_t swz64(int r, int ch) { return static_cast<ui
 
 // The partial slots of pieces i0 .. i1 - 1 (every `step`-th) of the unit whose first piece is CTA f's,
 // joined by `nthr` threads: into the unit's rows, or (unnormalised) into the slot of piece i0.
-template <int D>
+template <int D, int RM>
 __device__ void join_pieces(const ChunkArgs& a, int f, int i0, int i1, int step, const RowPiece& pc, bool last, int tid,
                             int nthr)
 {
@@ -170,12 +172,12 @@ __device__ void join_pieces(const ChunkArgs& a, int f, int i0, int i1, int step,
     }
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(RTHREADS, RCfg<D, FP8>::CTAS)
+template <int D, bool FP8, int NMT>
+__global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>::CTAS)
     chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, ChunkArgs a)
 {
-    using C = RCfg<D, FP8>;
-    constexpr int KS = D / 16, DT = D / 8, STAGES = C::STAGES;
+    using C = RCfg<D, FP8, NMT>;
+    constexpr int KS = D / 16, DT = D / 8, STAGES = C::STAGES, RM = C::RM, RW = C::RW;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* s_o = reinterpret_cast<float*>(smem + C::OFF_O);
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(RTHREADS, RCfg<D, FP8>::CTAS)
         keys = take > 0 ? max(s.len - s.n + take, 0) : 0;  // up to the last computed token
         return s;
     };
-    for (int b = threadIdx.x; b < p.B; b += RTHREADS) {
+    for (int b = threadIdx.x; b < p.B; b += C::THREADS) {
         int take, keys;
         const PagedSeq s = seq(b, p.cu[b], p.cu[b + 1], p.seq_lens[b], take, keys);
         if (c == 0 && (s.bad || s.n > a.max_q)) report_status(p.dev_status, KVATTN_STATUS_BAD_LENGTH);
@@ -393,7 +395,8 @@ __global__ void __launch_bounds__(RTHREADS, RCfg<D, FP8>::CTAS)
 
     // ===== consumers =====
     const int r0 = lane >> 2, cq = lane & 3;
-    const int tok0 = warp * 16;  // this warp's keys of a tile
+    const int mt = warp >> 2, sub = warp & 3;
+    const int tok0 = sub * 16;  // this warp's keys of a tile
     const int mi = lane >> 3, rr = lane & 7;
     const float sl2 = a.scale * kLog2e;
     int gs = 0;
@@ -409,15 +412,16 @@ __global__ void __launch_bounds__(RTHREADS, RCfg<D, FP8>::CTAS)
         {
             const bool have = warp_wait(&q_full[np & 1], (np / 2) & 1, s_abort);
             const uint8_t* sq = smem + C::OFF_Q + (np & 1) * C::QB;
-            const bool va = have && r0 < rows, vb = have && r0 + 8 < rows;
+            const int ra = mt * 16 + r0, rb = ra + 8;
+            const bool va = have && ra < rows, vb = have && rb < rows;
             if constexpr (FP8) {
                 // k step 4 h + s of thread cq: columns 64 h + 16 cq + 4 s + {0, 1 | 2, 3}
                 float m0 = 0.f, m1 = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     const int col = (ks >> 2) * 64 + cq * 16 + (ks & 3) * 4;
-                    const uint2 x = va ? *reinterpret_cast<const uint2*>(sq + (r0 * D + col) * 2) : make_uint2(0, 0);
-                    const uint2 y = vb ? *reinterpret_cast<const uint2*>(sq + ((r0 + 8) * D + col) * 2) : make_uint2(0, 0);
+                    const uint2 x = va ? *reinterpret_cast<const uint2*>(sq + (ra * D + col) * 2) : make_uint2(0, 0);
+                    const uint2 y = vb ? *reinterpret_cast<const uint2*>(sq + (rb * D + col) * 2) : make_uint2(0, 0);
                     qa[ks][0] = x.x;
                     qa[ks][1] = y.x;
                     qa[ks][2] = x.y;
@@ -447,16 +451,16 @@ __global__ void __launch_bounds__(RTHREADS, RCfg<D, FP8>::CTAS)
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     const int col = ks * 16 + 2 * cq;
-                    qa[ks][0] = va ? *reinterpret_cast<const uint32_t*>(sq + (r0 * D + col) * 2) : 0u;
-                    qa[ks][1] = vb ? *reinterpret_cast<const uint32_t*>(sq + ((r0 + 8) * D + col) * 2) : 0u;
-                    qa[ks][2] = va ? *reinterpret_cast<const uint32_t*>(sq + (r0 * D + col + 8) * 2) : 0u;
-                    qa[ks][3] = vb ? *reinterpret_cast<const uint32_t*>(sq + ((r0 + 8) * D + col + 8) * 2) : 0u;
+                    qa[ks][0] = va ? *reinterpret_cast<const uint32_t*>(sq + (ra * D + col) * 2) : 0u;
+                    qa[ks][1] = vb ? *reinterpret_cast<const uint32_t*>(sq + (rb * D + col) * 2) : 0u;
+                    qa[ks][2] = va ? *reinterpret_cast<const uint32_t*>(sq + (ra * D + col + 8) * 2) : 0u;
+                    qa[ks][3] = vb ? *reinterpret_cast<const uint32_t*>(sq + (rb * D + col + 8) * 2) : 0u;
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_empty[np & 1]);
         }
-        const int pos_a = pc.pos0 + (r0 >> gs), pos_b = pc.pos0 + ((r0 + 8) >> gs);
+        const int pos_a = pc.pos0 + ((mt * 16 + r0) >> gs), pos_b = pc.pos0 + ((mt * 16 + r0 + 8) >> gs);
         float o[DT][4];
 #pragma unroll
         for (int i = 0; i < DT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(RTHREADS, RCfg<D, FP8>::CTAS)
             if (have) {
                 const uint8_t* kt = smem + s * C::STAGE;
                 const uint8_t* vt = kt + C::TILE;
-                const uint32_t bad = s_bad[s] >> warp & 1u;  // this warp's 16 keys have no page
+                const uint32_t bad = s_bad[s] >> sub & 1u;  // this warp's 16 keys have no page
                 const int nv = pc.keys - t * RK - tok0;      // keys of this warp's that are in use
                 float sc[2][4];
 #pragma unroll
@@ -497,7 +501,7 @@ __global__ void __launch_bounds__(RTHREADS, RCfg<D, FP8>::CTAS)
                 }
                 // ---- scores in log2 units; keys past a row's position (or without a page) -> -inf ----
                 const int k0 = t * RK + tok0 + 2 * cq;
-                const bool masked = bad || t * RK + tok0 + 15 > pc.pos0;
+                const bool masked = bad || t * RK + tok0 + 15 > pc.pos0 + ((mt * 16) >> gs);
                 float zc[2][4];  // the scores with the values' scales (FP8)
                 float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
@@ -626,20 +630,20 @@ __global__ void __launch_bounds__(RTHREADS, RCfg<D, FP8>::CTAS)
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
         if (cq == 0) {
-            s_ml[warp * RM + r0] = make_float2(m0, l0);
-            s_ml[warp * RM + r0 + 8] = make_float2(m1, l1);
+            s_ml[warp * 16 + r0] = make_float2(m0, l0);
+            s_ml[warp * 16 + r0 + 8] = make_float2(m1, l1);
         }
         named_bar_sync(1, RW * 32);
         float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
 #pragma unroll
-        for (int j = 0; j < RW; ++j) {
-            M0 = fmaxf(M0, s_ml[j * RM + r0].x);
-            M1 = fmaxf(M1, s_ml[j * RM + r0 + 8].x);
+        for (int j = 0; j < 4; ++j) {
+            M0 = fmaxf(M0, s_ml[(mt * 4 + j) * 16 + r0].x);
+            M1 = fmaxf(M1, s_ml[(mt * 4 + j) * 16 + r0 + 8].x);
         }
         const float mu0 = M0 == -INFINITY ? 0.f : M0, mu1 = M1 == -INFINITY ? 0.f : M1;
 #pragma unroll
-        for (int j = 0; j < RW; ++j) {
-            const float2 x = s_ml[j * RM + r0], y = s_ml[j * RM + r0 + 8];
+        for (int j = 0; j < 4; ++j) {
+            const float2 x = s_ml[(mt * 4 + j) * 16 + r0], y = s_ml[(mt * 4 + j) * 16 + r0 + 8];
             L0 += fast_exp2(x.x - mu0) * x.y;
             L1 += fast_exp2(y.x - mu1) * y.y;
         }
@@ -671,23 +675,24 @@ __global__ void __launch_bounds__(RTHREADS, RCfg<D, FP8>::CTAS)
                     o[i][2 + e] += so[(r0 + 8) * C::SCR + col(i, e)];
                 }
         };
-        if (warp >= 2) spill(s_o + (warp - 2) * RM * C::SCR);
+        float* so = s_o + (mt * 2 + (sub & 1)) * 16 * C::SCR;
+        if (sub >= 2) spill(so);
         named_bar_sync(1, RW * 32);
-        if (warp < 2) fill(s_o + warp * RM * C::SCR);
-        if (warp < 2) spill(s_o + warp * RM * C::SCR);
-        if (warp == 0 && cq == 0) {
-            s_ml[r0] = make_float2(M0, L0);  // (every warp has read the sums)
-            s_ml[r0 + 8] = make_float2(M1, L1);
+        if (sub < 2) fill(so);
+        if (sub < 2) spill(so);
+        if (sub == 0 && cq == 0) {
+            s_ml[warp * 16 + r0] = make_float2(M0, L0);  // (every warp has read the sums)
+            s_ml[warp * 16 + r0 + 8] = make_float2(M1, L1);
         }
         named_bar_sync(1, RW * 32);
         // ---- the rows: finished, or a partial ----
         const long long slot = static_cast<long long>(2 * c + (c == pc.first ? 1 : 0)) * RM;
         for (int idx = threadIdx.x; idx < rows * (D / 4); idx += RW * 32) {
             const int r = idx / (D / 4), q4 = idx - r * (D / 4);
-            const float4 x = *reinterpret_cast<const float4*>(s_o + r * C::SCR + 4 * q4);
-            const float4 y = *reinterpret_cast<const float4*>(s_o + (RM + r) * C::SCR + 4 * q4);
+            const float* sr = s_o + ((r >> 4) * 32 + (r & 15)) * C::SCR + 4 * q4;
+            const float4 x = *reinterpret_cast<const float4*>(sr), y = *reinterpret_cast<const float4*>(sr + 16 * C::SCR);
             const float4 v = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-            const float2 ml = s_ml[r];
+            const float2 ml = s_ml[(r >> 4) * 64 + (r & 15)];
             if (pc.count == 1) {
                 const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
                 const long long row = static_cast<long long>(pc.t0 + (r >> gs)) * a.H + static_cast<long long>(pc.kvh) * a.g + (r & (a.g - 1));
@@ -728,7 +733,7 @@ __global__ void __launch_bounds__(RTHREADS, RCfg<D, FP8>::CTAS)
         bool go = *s_join;
         named_bar_sync(1, RW * 32);
         if (!go) continue;
-        join_pieces<D>(a, s.first, i0, i1, 1, s, groups == 1, threadIdx.x, RW * 32);
+        join_pieces<D, RM>(a, s.first, i0, i1, 1, s, groups == 1, threadIdx.x, RW * 32);
         if (groups == 1) continue;
         named_bar_sync(1, RW * 32);  // everyone has read the group's (m, l)
         const long long lead = static_cast<long long>(i0 == 0 ? 2 * s.first + 1 : 2 * (s.first + i0)) * RM;
@@ -746,27 +751,35 @@ __global__ void __launch_bounds__(RTHREADS, RCfg<D, FP8>::CTAS)
         named_bar_sync(1, RW * 32);
         go = *s_join;
         named_bar_sync(1, RW * 32);
-        if (go) join_pieces<D>(a, s.first, 0, s.count, RGROUP, s, true, threadIdx.x, RW * 32);
+        if (go) join_pieces<D, RM>(a, s.first, 0, s.count, RGROUP, s, true, threadIdx.x, RW * 32);
     }
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int NMT>
 cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
                          cudaStream_t stream)
 {
-    using C = RCfg<D, FP8>;
+    using C = RCfg<D, FP8, NMT>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(chunk_rows_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        e = cudaFuncSetAttribute(chunk_rows_kernel<D, FP8, NMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
     int grid = num_sms * C::CTAS;
     if (grid > CHUNK_MAX_SLOTS) grid = CHUNK_MAX_SLOTS;
-    return launch_pdl(chunk_rows_kernel<D, FP8>, dim3(grid), dim3(RTHREADS), C::SMEM, stream, tm_k, tm_v, a);
+    return launch_pdl(chunk_rows_kernel<D, FP8, NMT>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tm_k, tm_v, a);
+}
+
+template <int D, bool FP8>
+cudaError_t launch_rows(const ChunkArgs& a, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
+                        cudaStream_t stream)
+{
+    return a.max_q * a.g <= 16 ? launch_typed<D, FP8, 1>(a, tm_k, tm_v, num_sms, stream)
+                               : launch_typed<D, FP8, 2>(a, tm_k, tm_v, num_sms, stream);
 }
 
 }  // namespace
@@ -775,10 +788,10 @@ cudaError_t launch_chunk_rows(const ChunkArgs& a, bool fp8, const CUtensorMap& t
                               cudaStream_t stream)
 {
     if (a.d == 128)
-        return fp8 ? launch_typed<128, true>(a, tm_k, tm_v, num_sms, stream)
-                   : launch_typed<128, false>(a, tm_k, tm_v, num_sms, stream);
-    return fp8 ? launch_typed<64, true>(a, tm_k, tm_v, num_sms, stream)
-               : launch_typed<64, false>(a, tm_k, tm_v, num_sms, stream);
+        return fp8 ? launch_rows<128, true>(a, tm_k, tm_v, num_sms, stream)
+                   : launch_rows<128, false>(a, tm_k, tm_v, num_sms, stream);
+    return fp8 ? launch_rows<64, true>(a, tm_k, tm_v, num_sms, stream)
+               : launch_rows<64, false>(a, tm_k, tm_v, num_sms, stream);
 }
 
 }  // namespace kvattn

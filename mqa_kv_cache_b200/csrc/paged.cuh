@@ -72,7 +72,7 @@ struct ChunkArgs {
 };
 constexpr int CHUNK_MAX_CTAS = 148;     // tile kernel: at most this many CTAs, with slots of 256 rows
 constexpr int CHUNK_SLOT_ROWS = 256;
-constexpr int CHUNK_FEW_ROWS = 16;      // row kernel: query rows of a (sequence, KV head), and of a slot
+constexpr int CHUNK_FEW_ROWS = 32;      // row kernel: query rows of a (sequence, KV head), and of a slot
 constexpr int CHUNK_MAX_SLOTS = 296;    // row kernel: at most this many CTAs
 static_assert(3 * CHUNK_MAX_SLOTS * 4 <= KVATTN_DECODE_WS_ZERO_BYTES, "counters");
 cudaError_t launch_chunk_rows(const ChunkArgs& a, bool fp8, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,

@@ -684,61 +684,98 @@ _lib.attn_chunk_paged.argtypes = _chunk_head + [_vp, _vp, _f32, _vp, _vp, _vp, _
 _lib.attn_chunk_paged_fp8.argtypes = _chunk_head + [_vp, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _sz, _vp, _vp]
 
 
-def _paged_need(dev, tensors):
-    """Each (tensor, dtype, name) a contiguous CUDA tensor of that type on device `dev`."""
-    for t, dtype, name in tensors:
-        _need(t, dtype, name)
-        _contig(t, name)
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on another device")
+# A decode step's kernels here run for a few microseconds, so these wrappers keep to one pass of cheap
+# checks and hand plain integers to the library; what fails a check goes to _paged_refuse for its error.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _paged_refuse(dev, t, dtype, name):
+    _need(t, dtype, name)
+    _contig(t, name)
+    raise ValueError(f"{name} is on another device")
+
+
+def _paged_ptr(dev, t, dtype, name):
+    """The address of a contiguous CUDA tensor of that type on device `dev`."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _paged_refuse(dev, t, dtype, name)
+    return t.data_ptr()
 
 
 def _paged_tokens(x, name):
-    """(token stride, device) of packed head vectors [n_tokens, heads, d]: heads contiguous, any
+    """(shape, token stride, device) of packed head vectors [n_tokens, heads, d]: heads contiguous, any
     token stride (slices of a fused projection).  The device has to be the current one."""
-    _need(x, torch.bfloat16, name)
+    if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or x.get_device() < 0:
+        _need(x, torch.bfloat16, name)
     if x.dim() != 3:
         raise ValueError(f"{name} must be [n_tokens, heads, head_dim]")
-    T, H, d = x.shape
+    shape = x.shape
+    T, H, d = shape
     st, sh, sd = x.stride()
     if (sd != 1 and d > 1) or (sh != d and H > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
     dev = x.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"{name} is not on the current device")
-    return (st if T > 1 else H * d), dev
+    return shape, (st if T > 1 else H * d), dev
 
 
-def _paged_sizes(cu, seq_lens, page_table, pages, name):
-    """(B, max_pages, n_pages, page_size) from a batch's tensors and its pages [n_pages, Hk, page, d]."""
-    if page_table.dim() != 2 or pages.dim() != 4:
-        raise ValueError(f"page_table must be [B, max_pages] and {name} [n_pages, n_kv_head, page_size, head_dim]")
+def _paged_batch(dev, cu, seq_lens, page_table):
+    """(addresses of a batch's tensors, B, max_pages)."""
+    i32 = torch.int32
+    ptrs = (None if cu is None else _paged_ptr(dev, cu, i32, "cu"), _paged_ptr(dev, seq_lens, i32, "seq_lens"),
+            _paged_ptr(dev, page_table, i32, "page_table"))
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
     B, max_pages = page_table.shape
     if seq_lens.numel() != B or (cu is not None and cu.numel() != B + 1):
         raise ValueError("seq_lens must hold B entries and cu B + 1")
-    return B, max_pages, pages.shape[0], pages.shape[2]
+    return ptrs, B, max_pages
 
 
-def _append_paged(fn, fp8, k_new, v_new, cu, seq_lens, page_table, caches, cos, sin, pair_style, dev_status):
-    k_st, dev = _paged_tokens(k_new, "k_new")
-    v_st, _ = _paged_tokens(v_new, "v_new")
-    i32, f32 = torch.int32, torch.float32
+def _paged_caches(dev, fp8, k, v, ks, vs, Hk, d):
+    """(addresses in the library's order, n_pages, page size) of a cache [n_pages, Hk, page, d] and its scales;
+    Hk None: any."""
+    kn, vn = ("k_codes", "v_codes") if fp8 else ("k_pages", "v_pages")
     rows = torch.uint8 if fp8 else torch.bfloat16
-    _paged_need(dev, [(cu, i32, "cu"), (seq_lens, i32, "seq_lens"), (page_table, i32, "page_table"), (cos, f32, "cos"),
-                      (sin, f32, "sin"), *((t, f32 if n.endswith("scales") else rows, n) for n, t in caches)])
-    pages = caches[0][1]
-    B, max_pages, n_pages, page = _paged_sizes(cu, seq_lens, page_table, pages, caches[0][0])
-    T, Hk, d = k_new.shape
-    for n, t in caches:
-        if t.shape != (pages.shape[:3] if n.endswith("scales") else pages.shape):
-            raise ValueError(f"inconsistent shape of {n}")
-    if v_new.shape != k_new.shape or pages.shape[1] != Hk or pages.shape[3] != d:
+    kp, vp = _paged_ptr(dev, k, rows, kn), _paged_ptr(dev, v, rows, vn)
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"{kn} must be [n_pages, n_kv_head, page_size, head_dim]")
+    if v.shape != shape:
+        raise ValueError(f"inconsistent shape of {vn}")
+    if shape[3] != d or (Hk is not None and shape[1] != Hk):
+        raise ValueError(f"inconsistent shape of {kn}")
+    if not fp8:
+        return (kp, vp), shape[0], shape[2]
+    f32 = torch.float32
+    ksp, vsp = _paged_ptr(dev, ks, f32, "k_scales"), _paged_ptr(dev, vs, f32, "v_scales")
+    if ks.shape != shape[:3] or vs.shape != shape[:3]:
+        raise ValueError("inconsistent shape of the scales")
+    return (kp, ksp, vp, vsp), shape[0], shape[2]
+
+
+def _status_ptr(dev, t):
+    return None if t is None else _paged_ptr(dev, t, torch.int32, "dev_status")
+
+
+def _append_paged(fn, fp8, k_new, v_new, cu, seq_lens, page_table, k, ks, v, vs, cos, sin, pair_style, dev_status):
+    shape, k_st, dev = _paged_tokens(k_new, "k_new")
+    v_shape, v_st, _ = _paged_tokens(v_new, "v_new")
+    T, Hk, d = shape
+    if v_shape != shape:
         raise ValueError("inconsistent append shapes")
+    (cu_p, len_p, pt_p), B, max_pages = _paged_batch(dev, cu, seq_lens, page_table)
+    caches, n_pages, page = _paged_caches(dev, fp8, k, v, ks, vs, Hk, d)
+    f32 = torch.float32
+    cos_p, sin_p = _paged_ptr(dev, cos, f32, "cos"), _paged_ptr(dev, sin, f32, "sin")
     if cos.dim() != 2 or cos.shape[1] * 2 != d or sin.shape != cos.shape:
         raise ValueError("tables must be [max_pos, d/2]")
-    _check(fn(_ptr(k_new), k_st, _ptr(v_new), v_st, _ptr(cu), _ptr(seq_lens), _ptr(page_table), B, T, Hk, d, page,
-              max_pages, n_pages, *(_ptr(t) for _, t in caches), _ptr(cos), _ptr(sin), cos.shape[0], pair_style,
-              _ptr(dev_status), _stream()))
+    rc = fn(k_new.data_ptr(), k_st, v_new.data_ptr(), v_st, cu_p, len_p, pt_p, B, T, Hk, d, page, max_pages, n_pages,
+            *caches, cos_p, sin_p, cos.shape[0], pair_style, _status_ptr(dev, dev_status), _raw_stream(dev))
+    if rc:
+        _check(rc)
 
 
 def kv_append_paged_rope(k_new, v_new, cu, seq_lens, page_table, k_pages, v_pages, cos, sin, pair_style=0,
@@ -747,17 +784,16 @@ def kv_append_paged_rope(k_new, v_new, cu, seq_lens, page_table, k_pages, v_page
     their sequences ([n_pages, Hk, page, d] bf16; page_table int32 [B, max_pages]); seq_lens int32
     [B] counts the rows with the new tokens, so sequence b's token i goes to row
     seq_lens[b] - n_b + i, which is also its rotation position."""
-    _append_paged(_lib.kv_append_paged_rope, False, k_new, v_new, cu, seq_lens, page_table,
-                  (("k_pages", k_pages), ("v_pages", v_pages)), cos, sin, pair_style, dev_status)
+    _append_paged(_lib.kv_append_paged_rope, False, k_new, v_new, cu, seq_lens, page_table, k_pages, None, v_pages, None,
+                  cos, sin, pair_style, dev_status)
 
 
 def kv_append_paged_rope_fp8(k_new, v_new, cu, seq_lens, page_table, k_codes, k_scales, v_codes, v_scales, cos, sin,
                              pair_style=0, dev_status=None):
     """kv_append_paged_rope into an FP8 cache: E4M3 codes uint8 [n_pages, Hk, page, d] and one fp32
     scale per row and head [n_pages, Hk, page], quantised as they are written."""
-    _append_paged(_lib.kv_append_paged_rope_fp8, True, k_new, v_new, cu, seq_lens, page_table,
-                  (("k_codes", k_codes), ("k_scales", k_scales), ("v_codes", v_codes), ("v_scales", v_scales)),
-                  cos, sin, pair_style, dev_status)
+    _append_paged(_lib.kv_append_paged_rope_fp8, True, k_new, v_new, cu, seq_lens, page_table, k_codes, k_scales,
+                  v_codes, v_scales, cos, sin, pair_style, dev_status)
 
 
 def kv_read_paged_fp8(k_codes, k_scales, v_codes, v_scales, page_table, seq_lens, k_out, v_out, dev_status=None):
@@ -765,59 +801,56 @@ def kv_read_paged_fp8(k_codes, k_scales, v_codes, v_scales, page_table, seq_lens
     caches k_out, v_out [B, Hk, T_max, d] (rows past a length stay as they were)."""
     _need(k_out, torch.bfloat16, "k_out")
     dev = k_out.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError("k_out is not on the current device")
-    _paged_need(dev, [(k_out, torch.bfloat16, "k_out"), (v_out, torch.bfloat16, "v_out"),
-                      (k_codes, torch.uint8, "k_codes"), (v_codes, torch.uint8, "v_codes"),
-                      (k_scales, torch.float32, "k_scales"), (v_scales, torch.float32, "v_scales"),
-                      (page_table, torch.int32, "page_table"), (seq_lens, torch.int32, "seq_lens")])
-    B, max_pages, n_pages, page = _paged_sizes(None, seq_lens, page_table, k_codes, "k_codes")
+    ko, vo = _paged_ptr(dev, k_out, torch.bfloat16, "k_out"), _paged_ptr(dev, v_out, torch.bfloat16, "v_out")
+    if k_out.dim() != 4 or v_out.shape != k_out.shape:
+        raise ValueError("k_out and v_out must be [B, n_kv_head, T_max, head_dim]")
     Bo, Hk, T_max, d = k_out.shape
-    if (v_codes.shape != k_codes.shape or k_scales.shape != k_codes.shape[:3] or v_scales.shape != k_scales.shape
-            or Bo != B or v_out.shape != k_out.shape or k_codes.shape[1] != Hk or k_codes.shape[3] != d):
+    (_, len_p, pt_p), B, max_pages = _paged_batch(dev, None, seq_lens, page_table)
+    (kp, ksp, vp, vsp), n_pages, page = _paged_caches(dev, True, k_codes, v_codes, k_scales, v_scales, Hk, d)
+    if Bo != B:
         raise ValueError("inconsistent read shapes")
-    _check(_lib.kv_read_paged_fp8(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(page_table),
-                                  _ptr(seq_lens), B, Hk, d, page, max_pages, n_pages, T_max, _ptr(k_out), _ptr(v_out),
-                                  _ptr(dev_status), _stream()))
+    rc = _lib.kv_read_paged_fp8(kp, ksp, vp, vsp, pt_p, len_p, B, Hk, d, page, max_pages, n_pages, T_max, ko, vo,
+                                _status_ptr(dev, dev_status), _raw_stream(dev))
+    if rc:
+        _check(rc)
 
 
 def attn_chunk_paged_workspace_bytes(B, n_tokens, max_q, n_head, n_kv_head, head_dim) -> int:
     return int(_lib.attn_chunk_paged_workspace_bytes(B, n_tokens, max_q, n_head, n_kv_head, head_dim))
 
 
-def _chunk_paged(fn, fp8, q, cu, seq_lens, page_table, caches, scale, max_q, out, lse, ws, dev_status, want_lse):
-    q_st, dev = _paged_tokens(q, "q")
-    i32, f32 = torch.int32, torch.float32
-    rows = torch.uint8 if fp8 else torch.bfloat16
-    _paged_need(dev, [(cu, i32, "cu"), (seq_lens, i32, "seq_lens"), (page_table, i32, "page_table"),
-                      *((t, f32 if n.endswith("scales") else rows, n) for n, t in caches)])
-    pages = caches[0][1]
-    B, max_pages, n_pages, page = _paged_sizes(cu, seq_lens, page_table, pages, caches[0][0])
-    T, H, d = q.shape
-    Hk = pages.shape[1]
-    for n, t in caches:
-        if t.shape != (pages.shape[:3] if n.endswith("scales") else pages.shape):
-            raise ValueError(f"inconsistent shape of {n}")
-    if pages.shape[3] != d:
-        raise ValueError("inconsistent chunk shapes")
+def _chunk_paged(fn, fp8, q, cu, seq_lens, page_table, k, ks, v, vs, scale, max_q, out, lse, ws, dev_status, want_lse):
+    shape, q_st, dev = _paged_tokens(q, "q")
+    T, H, d = shape
+    (cu_p, len_p, pt_p), B, max_pages = _paged_batch(dev, cu, seq_lens, page_table)
+    caches, n_pages, page = _paged_caches(dev, fp8, k, v, ks, vs, None, d)
+    Hk = k.shape[1]
     if out is None:
-        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out_p = out.data_ptr()
     else:
-        _paged_need(dev, [(out, torch.bfloat16, "out")])
-        if out.shape != q.shape:
+        out_p = _paged_ptr(dev, out, torch.bfloat16, "out")
+        if out.shape != shape:
             raise ValueError("out must have the shape of q")
     if lse is not None:
-        _paged_need(dev, [(lse, f32, "lse")])
+        lse_p = _paged_ptr(dev, lse, torch.float32, "lse")
         if lse.shape != (T, H):
             raise ValueError("lse must be [n_tokens, n_head]")
     elif want_lse:
-        lse = torch.empty((T, H), dtype=f32, device=q.device)
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse_p = lse.data_ptr()
+    else:
+        lse_p = None
     max_q = 0 if max_q is None else int(max_q)
     if ws is None:
         ws = workspace(attn_chunk_paged_workspace_bytes(B, T, max_q, H, Hk, d), q.device)
-    _check(fn(_ptr(q), q_st, _ptr(cu), _ptr(seq_lens), _ptr(page_table), B, T, max_q, H, Hk, d, page, max_pages,
-              n_pages, *(_ptr(t) for _, t in caches), float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-              _ptr(dev_status), _stream()))
+    rc = fn(q.data_ptr(), q_st, cu_p, len_p, pt_p, B, T, max_q, H, Hk, d, page, max_pages, n_pages, *caches, float(scale),
+            out_p, lse_p, _paged_ptr(dev, ws, torch.uint8, "ws"), ws.numel(), _status_ptr(dev, dev_status),
+            _raw_stream(dev))
+    if rc:
+        _check(rc)
     return out, lse
 
 
@@ -828,13 +861,12 @@ def attn_chunk_paged(q, cu, seq_lens, page_table, k_pages, v_pages, scale, max_q
     cu int32 [B + 1], seq_lens int32 [B] (rows with the new tokens), page_table int32
     [B, max_pages], pages [n_pages, Hk, page, d] -> (out [n_tokens, H, d] bf16, lse [n_tokens, H]
     fp32 or None).  max_q: an upper bound of the chunk lengths known to the host."""
-    return _chunk_paged(_lib.attn_chunk_paged, False, q, cu, seq_lens, page_table,
-                        (("k_pages", k_pages), ("v_pages", v_pages)), scale, max_q, out, lse, ws, dev_status, want_lse)
+    return _chunk_paged(_lib.attn_chunk_paged, False, q, cu, seq_lens, page_table, k_pages, None, v_pages, None, scale,
+                        max_q, out, lse, ws, dev_status, want_lse)
 
 
 def attn_chunk_paged_fp8(q, cu, seq_lens, page_table, k_codes, k_scales, v_codes, v_scales, scale, max_q=None,
                          out=None, lse=None, ws=None, dev_status=None, want_lse=True):
     """attn_chunk_paged over an FP8 cache (kv_append_paged_rope_fp8)."""
-    return _chunk_paged(_lib.attn_chunk_paged_fp8, True, q, cu, seq_lens, page_table,
-                        (("k_codes", k_codes), ("k_scales", k_scales), ("v_codes", v_codes), ("v_scales", v_scales)),
-                        scale, max_q, out, lse, ws, dev_status, want_lse)
+    return _chunk_paged(_lib.attn_chunk_paged_fp8, True, q, cu, seq_lens, page_table, k_codes, k_scales, v_codes,
+                        v_scales, scale, max_q, out, lse, ws, dev_status, want_lse)
