@@ -105,9 +105,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 }
 
 // Map of [z][y][x] with byte strides, boxes 128 bytes wide (64 bf16, 128-byte swizzle) or, over
-// bytes, `box_x` wide (64: 64-byte swizzle, else none); what lies outside reads as zero.
+// bytes, `byte_box_x` wide; the swizzle is given for bytes.  What lies outside reads as zero.
 int encode_map(const char* name, CUtensorMap* map, const void* base, uint32_t byte_box_x, uint64_t x, uint64_t y,
-               uint64_t z, uint64_t y_stride, uint64_t z_stride, uint32_t box_y, uint32_t box_z, bool swizzle64 = false)
+               uint64_t z, uint64_t y_stride, uint64_t z_stride, uint32_t box_y, uint32_t box_z,
+               CUtensorMapSwizzle byte_swizzle = CU_TENSOR_MAP_SWIZZLE_NONE)
 {
     auto fn = encode_fn();
     if (!fn) return record_error(KVATTN_ERR_CUDA, "%s: cuTensorMapEncodeTiled is unavailable", name);
@@ -116,9 +117,7 @@ int encode_map(const char* name, CUtensorMap* map, const void* base, uint32_t by
     const cuuint32_t box[3] = {bytes ? byte_box_x : 64u, box_y, box_z}, one[3] = {1, 1, 1};
     const CUresult r = fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                           const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          !bytes      ? CU_TENSOR_MAP_SWIZZLE_128B
-                          : swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                      : CU_TENSOR_MAP_SWIZZLE_NONE,
+                          bytes ? byte_swizzle : CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return record_error(KVATTN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", name, static_cast<int>(r));
@@ -234,10 +233,13 @@ int chunk(const char* name, bool fp8, const kvattn_bf16* q, int64_t q_stride, co
     a.part_o = reinterpret_cast<float*>(wp + ws.o);
     const uint64_t row = head_dim * (fp8 ? 1 : 2), planes = static_cast<uint64_t>(n_pages) * n_kv_head;
     const uint32_t tile = few ? 64 : 128, box = page_size < static_cast<int>(tile) ? page_size : tile;
-    const uint32_t byte_box = fp8 ? (few ? 64 : head_dim) : 0;
+    const uint32_t byte_box = fp8 ? head_dim : 0;
+    const CUtensorMapSwizzle sw = !few             ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                  : head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                    : CU_TENSOR_MAP_SWIZZLE_64B;
     CUtensorMap mq, mk, mv;
-    if ((rc = encode_map(name, &mk, k_pages, byte_box, head_dim, page_size, planes, row, row * page_size, box, 1, few)) != KVATTN_OK ||
-        (rc = encode_map(name, &mv, v_pages, byte_box, head_dim, page_size, planes, row, row * page_size, box, 1, few)) != KVATTN_OK)
+    if ((rc = encode_map(name, &mk, k_pages, byte_box, head_dim, page_size, planes, row, row * page_size, box, 1, sw)) != KVATTN_OK ||
+        (rc = encode_map(name, &mv, v_pages, byte_box, head_dim, page_size, planes, row, row * page_size, box, 1, sw)) != KVATTN_OK)
         return rc;
     if (few) return finish(kvattn::launch_chunk_rows(a, fp8, mk, mv, sms, static_cast<cudaStream_t>(stream)), name);
     if ((rc = encode_map(name, &mq, q, 0, head_dim, n_head, n_tokens, head_dim * 2, q_stride * 2, g, 128 / g)) != KVATTN_OK)

@@ -55,8 +55,9 @@ struct RCfg {
     static constexpr int RW = 4 * NMT;
     static constexpr int THREADS = 32 * (RW + 2);
     static constexpr int CTAS = FP8 && NMT == 1 ? 2 : 1;  // per SM
-    static constexpr int HALVES = D / 64;
-    static constexpr int ROWB = FP8 ? 64 : 128;       // bytes of a 64-column row in shared memory
+    static constexpr int ROWB = D * (FP8 ? 1 : 2) < 128 ? 64 : 128;  // bytes of a row of a box, and its swizzle
+    static constexpr int HALVES = D * (FP8 ? 1 : 2) / ROWB;           // boxes side by side
+    static constexpr int BOXD = D / HALVES;                           // columns of one
     static constexpr int BOX = RK * ROWB;
     static constexpr int TILE = HALVES * BOX;          // K or V
     static constexpr int SCB = FP8 ? 2 * RK * 4 : 0;   // their scales
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>:
                     const int z = bad ? oob : e * a.Hk + pc.kvh;
                     const int y = row & ((1 << p.page_shift) - 1);
                     tma_load_3d_hint(smem + s * C::STAGE + (is_v ? C::TILE : 0) + half * C::BOX + (box << bp_shift) * C::ROWB,
-                                     is_v ? &tm_v : &tm_k, &full[s], half * 64, y, z, pol);
+                                     is_v ? &tm_v : &tm_k, &full[s], half * C::BOXD, y, z, pol);
                     if (FP8 && half == 0 && !bad)
                         bulk_load(smem + C::OFF_SC + s * C::SCB + (is_v ? RK * 4 : 0) + (box << bp_shift) * 4,
                                   (is_v ? a.v_scales : a.k_scales) + ((static_cast<long long>(z) << p.page_shift) + y), bp * 4,
@@ -480,10 +481,21 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>:
                 if constexpr (FP8) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
+                        // D = 128: odd keys read their upper 64 codes first, so that two keys' reads
+                        // fall on different banks
+                        uint4 k4[D / 64];
+                        if constexpr (D == 128) {
+                            const int row = tok0 + i * 8 + r0, odd = r0 & 1;
+                            const uint4 x = *reinterpret_cast<const uint4*>(kt + swz128(row, odd * 4 + cq));
+                            const uint4 y = *reinterpret_cast<const uint4*>(kt + swz128(row, (odd ^ 1) * 4 + cq));
+                            k4[0] = odd ? y : x;
+                            k4[D / 64 - 1] = odd ? x : y;
+                        } else {
+                            k4[0] = *reinterpret_cast<const uint4*>(kt + swz64(tok0 + i * 8 + r0, cq));
+                        }
 #pragma unroll
-                        for (int h = 0; h < C::HALVES; ++h) {
-                            const uint4 k4 = *reinterpret_cast<const uint4*>(kt + h * C::BOX + swz64(tok0 + i * 8 + r0, cq));
-                            const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+                        for (int h = 0; h < D / 64; ++h) {
+                            const uint32_t kw[4] = {k4[h].x, k4[h].y, k4[h].z, k4[h].w};
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
                                 mma_f16_16816(sc[i], qa[h * 4 + x], codes_to_f16x2(kw[x]), codes_to_f16x2(kw[x] >> 16));
@@ -587,9 +599,9 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>:
 #pragma unroll
                     for (int dg = 0; dg < D / 32; ++dg) {
                         // keys 0-7 | 8-15 of 16 columns, and of the next 16
-                        const int ch = (dg * 2 + (mi >> 1)) & 3;
+                        const int ch = dg * 2 + (mi >> 1);
                         uint32_t v[4];
-                        ldsm_x4_t(smem_u32(vt) + (dg >> 1) * C::BOX + swz64(vrow, ch), v[0], v[1], v[2], v[3]);
+                        ldsm_x4_t(smem_u32(vt) + (D == 128 ? swz128(vrow, ch) : swz64(vrow, ch)), v[0], v[1], v[2], v[3]);
                         if (tail) {
                             v[0] &= z0;
                             v[2] &= z0;
