@@ -13,8 +13,8 @@
 // an unnormalised partial and the CTA that finishes last joins them, in groups of 16
 // pieces and then the groups, always in the same order.
 //
-// Four warps per 16 query rows: 16 keys of every tile each, with their own running maximum
-// and sum, joined at the end of a piece.  One warp loads (one box per page and 64-column
+// Four warps per 16 query rows: 32 keys of every other tile each, with their own running
+// maximum and sum, joined at the end of a piece.  One warp loads (one box per page and 64-column
 // half, page entries fetched one tile ahead; the piece's query rows), the last one makes
 // the pieces.
 //
@@ -62,7 +62,8 @@ struct RCfg {
     static constexpr int TILE = HALVES * BOX;          // K or V
     static constexpr int SCB = FP8 ? 2 * RK * 4 : 0;   // their scales
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int STAGES = (FP8 ? (NMT == 1 ? 4 : 8) : 5) * (D == 128 ? 1 : 2);
+    static constexpr int STAGES = (FP8 ? (NMT == 1 ? 4 : 8) : (NMT == 1 ? 6 : 4)) * (D == 128 ? 1 : 2);
+    static_assert(STAGES % 2 == 0, "a stage always holds even tiles or always odd ones: its barriers count one half of the warps");
     static constexpr int SCR = D + 8;                  // floats per scratch row
     static constexpr int OFF_SC = STAGES * STAGE;
     static constexpr int OFF_Q = OFF_SC + STAGES * SCB;  // two pieces' query rows
@@ -107,6 +108,12 @@ __device__ __forceinline__ float lg2(float x)
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// warp_wait with a first look that asks for the phase alone.
+__device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity, volatile int* abort_flag)
+{
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || warp_wait(bar, parity, abort_flag);
 }
 
 // Byte offset of 16-byte chunk `ch` (of 4) of row r in a 64-byte-swizzled block of 64-byte rows.
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>:
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], RW);
+            mbar_init(&empty[i], RW / 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
@@ -397,7 +404,8 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>:
     // ===== consumers =====
     const int r0 = lane >> 2, cq = lane & 3;
     const int mt = warp >> 2, sub = warp & 3;
-    const int tok0 = sub * 16;  // this warp's keys of a tile
+    const uint32_t turn = sub >> 1;   // even or odd tiles
+    const int tok0 = (sub & 1) * 32;  // this warp's keys of a tile
     const int mi = lane >> 3, rr = lane & 7;
     const float sl2 = a.scale * kLog2e;
     int gs = 0;
@@ -468,98 +476,102 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>:
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
         for (int t = pc.tb; t < pc.te; ++t, ++it) {
+            if ((it & 1) != turn) continue;
             const uint32_t s = it % STAGES;
-            const bool have = warp_wait(&full[s], (it / STAGES) & 1, s_abort);
-            if (have) {
+            if (ready(&full[s], (it / STAGES) & 1, s_abort)) {
                 const uint8_t* kt = smem + s * C::STAGE;
                 const uint8_t* vt = kt + C::TILE;
-                const uint32_t bad = s_bad[s] >> sub & 1u;  // this warp's 16 keys have no page
-                const int nv = pc.keys - t * RK - tok0;      // keys of this warp's that are in use
-                float sc[2][4];
+                const uint32_t bad = s_bad[s] >> (tok0 / 16) & 3u;  // this warp's groups of 16 keys without a page
+                const int nv = pc.keys - t * RK - tok0;             // keys of this warp's that are in use
+                float sc[4][4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+                for (int i = 0; i < 4; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
                 if constexpr (FP8) {
+                    // D = 128: odd keys read their upper 64 codes first, so that two keys' reads fall
+                    // on different banks
+                    const int odd = r0 & 1;
+                    uint4 k4[4][D / 64];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        // D = 128: odd keys read their upper 64 codes first, so that two keys' reads
-                        // fall on different banks
-                        uint4 k4[D / 64];
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = tok0 + i * 8 + r0;
                         if constexpr (D == 128) {
-                            const int row = tok0 + i * 8 + r0, odd = r0 & 1;
                             const uint4 x = *reinterpret_cast<const uint4*>(kt + swz128(row, odd * 4 + cq));
                             const uint4 y = *reinterpret_cast<const uint4*>(kt + swz128(row, (odd ^ 1) * 4 + cq));
-                            k4[0] = odd ? y : x;
-                            k4[D / 64 - 1] = odd ? x : y;
+                            k4[i][0] = odd ? y : x;
+                            k4[i][D / 64 - 1] = odd ? x : y;
                         } else {
-                            k4[0] = *reinterpret_cast<const uint4*>(kt + swz64(tok0 + i * 8 + r0, cq));
-                        }
-#pragma unroll
-                        for (int h = 0; h < D / 64; ++h) {
-                            const uint32_t kw[4] = {k4[h].x, k4[h].y, k4[h].z, k4[h].w};
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                mma_f16_16816(sc[i], qa[h * 4 + x], codes_to_f16x2(kw[x]), codes_to_f16x2(kw[x] >> 16));
+                            k4[i][0] = *reinterpret_cast<const uint4*>(kt + swz64(row, cq));
                         }
                     }
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t kw = x == 0 ? k4[i][h].x : x == 1 ? k4[i][h].y : x == 2 ? k4[i][h].z : k4[i][h].w;
+                                mma_f16_16816(sc[i], qa[h * 4 + x], codes_to_f16x2(kw), codes_to_f16x2(kw >> 16));
+                            }
                 } else {
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
                         const int dim = ks * 16 + ((mi & 1) << 3);
-                        uint32_t b0, b1, b2, b3;
-                        ldsm_x4(smem_u32(kt) + (dim >> 6) * C::BOX + swz128(tok0 + rr + ((mi >> 1) << 3), (dim & 63) >> 3), b0, b1, b2, b3);
-                        mma_bf16_16816(sc[0], qa[ks], b0, b1);
-                        mma_bf16_16816(sc[1], qa[ks], b2, b3);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t b0, b1, b2, b3;
+                            ldsm_x4(smem_u32(kt) + (dim >> 6) * C::BOX +
+                                        swz128(tok0 + j * 16 + rr + ((mi >> 1) << 3), (dim & 63) >> 3),
+                                    b0, b1, b2, b3);
+                            mma_bf16_16816(sc[2 * j], qa[ks], b0, b1);
+                            mma_bf16_16816(sc[2 * j + 1], qa[ks], b2, b3);
+                        }
                     }
                 }
                 // ---- scores in log2 units; keys past a row's position (or without a page) -> -inf ----
-                const int k0 = t * RK + tok0 + 2 * cq;
-                const bool masked = bad || t * RK + tok0 + 15 > pc.pos0 + ((mt * 16) >> gs);
-                float zc[2][4];  // the scores with the values' scales (FP8)
+                const bool masked = bad || t * RK + tok0 + 31 > pc.pos0 + ((mt * 16) >> gs);
+                float2 lv[4];  // log2 of the values' scales (FP8)
                 float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float2 kv = make_float2(1.f, 1.f), lv = make_float2(0.f, 0.f);
+                for (int i = 0; i < 4; ++i) {
+                    float2 kv = make_float2(1.f, 1.f);
                     if constexpr (FP8) {
                         const float* scl = reinterpret_cast<const float*>(smem + C::OFF_SC + s * C::SCB) + tok0 + i * 8 + 2 * cq;
                         kv = *reinterpret_cast<const float2*>(scl);
                         const float2 v = *reinterpret_cast<const float2*>(scl + RK);
-                        lv = make_float2(lg2(v.x), lg2(v.y));  // a zero row: -inf, its weight 0
+                        lv[i] = make_float2(lg2(v.x), lg2(v.y));  // a zero row: -inf, its weight 0
                     }
                     sc[i][0] *= qs0 * kv.x;
                     sc[i][1] *= qs0 * kv.y;
                     sc[i][2] *= qs1 * kv.x;
                     sc[i][3] *= qs1 * kv.y;
-                    if (FP8) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) zc[i][e] = sc[i][e] + ((e & 1) ? lv.y : lv.x);
-                    }
                     if (masked) {
+                        const int k = t * RK + tok0 + i * 8 + 2 * cq;
+                        const bool b = bad >> (i >> 1) & 1u;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (bad || k0 + i * 8 + (e & 1) > (e < 2 ? pos_a : pos_b)) {
-                                sc[i][e] = -INFINITY;
-                                if (FP8) zc[i][e] = -INFINITY;
-                            }
+                        for (int e = 0; e < 4; ++e)
+                            if (b || k + (e & 1) > (e < 2 ? pos_a : pos_b)) sc[i][e] = -INFINITY;
+                        if (FP8) {  // such a key's scale may be anything, NaN included
+                            if (b || k >= pc.keys) lv[i].x = 0.f;
+                            if (b || k + 1 >= pc.keys) lv[i].y = 0.f;
                         }
                     }
                     if constexpr (FP8) {
                         // the sums use the same reference as the weighted values: it may lie below the largest
                         // score (rows of tiny scale), but by no more than fp32 holds
-                        mx0 = fmaxf(mx0, fmaxf(fmaxf(zc[i][0], zc[i][1]), fmaxf(sc[i][0], sc[i][1]) - 100.f));
-                        mx1 = fmaxf(mx1, fmaxf(fmaxf(zc[i][2], zc[i][3]), fmaxf(sc[i][2], sc[i][3]) - 100.f));
+                        mx0 = fmaxf(mx0, fmaxf(fmaxf(sc[i][0] + lv[i].x, sc[i][1] + lv[i].y), fmaxf(sc[i][0], sc[i][1]) - 100.f));
+                        mx1 = fmaxf(mx1, fmaxf(fmaxf(sc[i][2] + lv[i].x, sc[i][3] + lv[i].y), fmaxf(sc[i][2], sc[i][3]) - 100.f));
                     } else {
                         mx0 = fmaxf(mx0, fmaxf(sc[i][0], sc[i][1]));
                         mx1 = fmaxf(mx1, fmaxf(sc[i][2], sc[i][3]));
                     }
                 }
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-                const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-                const float mu0 = mn0 == -INFINITY ? 0.f : mn0, mu1 = mn1 == -INFINITY ? 0.f : mn1;
-                if (__any_sync(0xffffffffu, mn0 > m0 || mn1 > m1)) {
-                    const float al0 = fast_exp2(m0 - mu0), al1 = fast_exp2(m1 - mu1);
+                if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
+                    const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+                    const float al0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - mn0), al1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mn1);
                     l0 *= al0;
                     l1 *= al1;
 #pragma unroll
@@ -572,63 +584,68 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>:
                     m0 = mn0;
                     m1 = mn1;
                 }
-                uint32_t pa[4];
+                const float mu0 = m0 == -INFINITY ? 0.f : m0, mu1 = m1 == -INFINITY ? 0.f : m1;
+                uint32_t pa[2][4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 4; ++i) {
                     float w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float x = fast_exp2(sc[i][e] - (e < 2 ? mu0 : mu1));
-                        if (e < 2) l0 += x;
-                        else l1 += x;
-                        w[e] = FP8 ? fast_exp2(zc[i][e] - (e < 2 ? mu0 : mu1)) : x;
+                        const float x = sc[i][e] - (e < 2 ? mu0 : mu1), y = fast_exp2(x);
+                        if (e < 2) l0 += y;
+                        else l1 += y;
+                        w[e] = FP8 ? fast_exp2(x + ((e & 1) ? lv[i].y : lv[i].x)) : y;
                     }
-                    pa[2 * i] = FP8 ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]);
-                    pa[2 * i + 1] = FP8 ? pack_f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]);
+                    pa[i >> 1][2 * (i & 1)] = FP8 ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]);
+                    pa[i >> 1][2 * (i & 1) + 1] = FP8 ? pack_f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]);
                 }
                 // ---- O += P V; rows behind the last key in use may hold anything: zeros instead ----
-                const bool tail = bad || nv < 16;
-                uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;
-                if (tail) {
-                    const int v0 = 2 * cq;
-                    z0 = bad ? 0u : (v0 < nv ? 0x0000ffffu : 0u) | (v0 + 1 < nv ? 0xffff0000u : 0u);
-                    z1 = bad ? 0u : (v0 + 8 < nv ? 0x0000ffffu : 0u) | (v0 + 9 < nv ? 0xffff0000u : 0u);
-                }
-                const int vrow = tok0 + rr + ((mi & 1) << 3);
-                if constexpr (FP8) {
 #pragma unroll
-                    for (int dg = 0; dg < D / 32; ++dg) {
-                        // keys 0-7 | 8-15 of 16 columns, and of the next 16
-                        const int ch = dg * 2 + (mi >> 1);
-                        uint32_t v[4];
-                        ldsm_x4_t(smem_u32(vt) + (D == 128 ? swz128(vrow, ch) : swz64(vrow, ch)), v[0], v[1], v[2], v[3]);
-                        if (tail) {
-                            v[0] &= z0;
-                            v[2] &= z0;
-                            v[1] &= z1;
-                            v[3] &= z1;
-                        }
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) v[x] = __byte_perm(v[x], 0u, 0x3120);  // even columns' pair | odd columns'
-                        mma_f16_16816(o[4 * dg], pa, codes_to_f16x2(v[0]), codes_to_f16x2(v[1]));
-                        mma_f16_16816(o[4 * dg + 1], pa, codes_to_f16x2(v[0] >> 16), codes_to_f16x2(v[1] >> 16));
-                        mma_f16_16816(o[4 * dg + 2], pa, codes_to_f16x2(v[2]), codes_to_f16x2(v[3]));
-                        mma_f16_16816(o[4 * dg + 3], pa, codes_to_f16x2(v[2] >> 16), codes_to_f16x2(v[3] >> 16));
+                for (int j = 0; j < 2; ++j) {
+                    const bool b = bad >> j & 1u;
+                    const bool tail = b || nv < j * 16 + 16;
+                    uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;
+                    if (tail) {
+                        const int v0 = j * 16 + 2 * cq;
+                        z0 = b ? 0u : (v0 < nv ? 0x0000ffffu : 0u) | (v0 + 1 < nv ? 0xffff0000u : 0u);
+                        z1 = b ? 0u : (v0 + 8 < nv ? 0x0000ffffu : 0u) | (v0 + 9 < nv ? 0xffff0000u : 0u);
                     }
-                } else {
+                    const int vrow = tok0 + j * 16 + rr + ((mi & 1) << 3);
+                    if constexpr (FP8) {
 #pragma unroll
-                    for (int dp = 0; dp < D / 16; ++dp) {
-                        const int dim = dp * 16 + ((mi >> 1) << 3);
-                        uint32_t v0, v1, v2, v3;
-                        ldsm_x4_t(smem_u32(vt) + (dim >> 6) * C::BOX + swz128(vrow, (dim & 63) >> 3), v0, v1, v2, v3);
-                        if (tail) {
-                            v0 &= z0;
-                            v2 &= z0;
-                            v1 &= z1;
-                            v3 &= z1;
+                        for (int dg = 0; dg < D / 32; ++dg) {
+                            // keys 0-7 | 8-15 of 16 columns, and of the next 16
+                            const int ch = dg * 2 + (mi >> 1);
+                            uint32_t v[4];
+                            ldsm_x4_t(smem_u32(vt) + (D == 128 ? swz128(vrow, ch) : swz64(vrow, ch)), v[0], v[1], v[2], v[3]);
+                            if (tail) {
+                                v[0] &= z0;
+                                v[2] &= z0;
+                                v[1] &= z1;
+                                v[3] &= z1;
+                            }
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) v[x] = __byte_perm(v[x], 0u, 0x3120);  // even columns' pair | odd columns'
+                            mma_f16_16816(o[4 * dg], pa[j], codes_to_f16x2(v[0]), codes_to_f16x2(v[1]));
+                            mma_f16_16816(o[4 * dg + 1], pa[j], codes_to_f16x2(v[0] >> 16), codes_to_f16x2(v[1] >> 16));
+                            mma_f16_16816(o[4 * dg + 2], pa[j], codes_to_f16x2(v[2]), codes_to_f16x2(v[3]));
+                            mma_f16_16816(o[4 * dg + 3], pa[j], codes_to_f16x2(v[2] >> 16), codes_to_f16x2(v[3] >> 16));
                         }
-                        mma_bf16_16816(o[2 * dp], pa, v0, v1);
-                        mma_bf16_16816(o[2 * dp + 1], pa, v2, v3);
+                    } else {
+#pragma unroll
+                        for (int dp = 0; dp < D / 16; ++dp) {
+                            const int dim = dp * 16 + ((mi >> 1) << 3);
+                            uint32_t v0, v1, v2, v3;
+                            ldsm_x4_t(smem_u32(vt) + (dim >> 6) * C::BOX + swz128(vrow, (dim & 63) >> 3), v0, v1, v2, v3);
+                            if (tail) {
+                                v0 &= z0;
+                                v2 &= z0;
+                                v1 &= z1;
+                                v3 &= z1;
+                            }
+                            mma_bf16_16816(o[2 * dp], pa[j], v0, v1);
+                            mma_bf16_16816(o[2 * dp + 1], pa[j], v2, v3);
+                        }
                     }
                 }
             }
