@@ -4,8 +4,10 @@
 // Method: out = softmax_{j <= p} (scale q . k_j) v_j for the query at position p, query
 // head h reading KV head h / g ("注意力变体与 MoE", GQA attention(): the g heads of a
 // group share one K/V); all rows of a (sequence, KV head), its tokens times g heads, 32
-// at most, are the M rows of one or two mma.sync tiles, so every cached row is read once
-// and the kernel is bound by that read.
+// at most, meet each cached row together, so every one is read once and the kernel is
+// bound by that read.  The products run on mma.sync with the keys (then the columns of V)
+// as M and 8 query rows as N: S^T = K Q^T, O^T = V^T P^T, so that 8 rows, a group of 8
+// heads decoding, waste nothing; P^T's fragments are S^T's, transposed (movmatrix).
 //
 // Work: the 64-key tiles of all (sequence, KV head) units form one line, dealt out to the
 // CTAs in equal stretches (as decode_plan.cuh does for contiguous caches); a stretch of a
@@ -13,18 +15,19 @@
 // an unnormalised partial and the CTA that finishes last joins them, in groups of 16
 // pieces and then the groups, always in the same order.
 //
-// Four warps per 16 query rows: 32 keys of every other tile each, with their own running
+// Four warps per 8 or 16 query rows: 32 keys of every other tile each, with their own running
 // maximum and sum, joined at the end of a piece.  One warp loads (one box per page and 64-column
 // half, page entries fetched one tile ahead; the piece's query rows), the last one makes
 // the pieces.
 //
 // FP8: the codes become fp16 in registers, one conversion for two of them (exact).  K: a
-// thread's 16 codes of a key are one load, the k order of the MMA being free as long as Q
+// thread's codes of a key are 16-byte loads, the k order of the MMA being free as long as Q
 // follows it; Q is scaled per row by a power of two into fp16's range (an element below
 // 2^-29 of its row's largest rounds to a multiple of 2^-40 of it, far below the fp32 sums'
-// own rounding).  V: transposed as pairs of bytes, the even and the odd columns of 16 being
-// two n-tiles.  Weights enter the product as 2^(s_j + log2 vs_j - m), so the values'
-// scales cost an addition and the product's largest weight is near 1 whatever they are.
+// own rounding).  V: transposed as pairs of bytes, the even columns of 16 being the first
+// eight rows of V^T's tile and the odd ones the others.  Weights enter the product as
+// 2^(s_j + log2 vs_j - m), so the values' scales cost an addition and the product's largest
+// weight is near 1 whatever they are.
 #include "common.cuh"
 #include "kernels.h"
 #include "paged.cuh"
@@ -48,10 +51,11 @@ struct RowPiece {
     int count;      // pieces of the unit
 };
 
-// NMT: 16-row tiles of query rows; each has four consumer warps
-template <int D, bool FP8, int NMT>
+// NQ: n-tiles of 8 query rows in a warp; NMT: sets of four warps, each with its own such rows.
+template <int D, bool FP8, int NQ, int NMT>
 struct RCfg {
-    static constexpr int RM = 16 * NMT;
+    static constexpr int WR = 8 * NQ;      // query rows of a set of warps
+    static constexpr int RM = WR * NMT;
     static constexpr int RW = 4 * NMT;
     static constexpr int THREADS = 32 * (RW + 2);
     static constexpr int CTAS = FP8 && NMT == 1 ? 2 : 1;  // per SM
@@ -68,9 +72,9 @@ struct RCfg {
     static constexpr int OFF_SC = STAGES * STAGE;
     static constexpr int OFF_Q = OFF_SC + STAGES * SCB;  // two pieces' query rows
     static constexpr int QB = RM * D * 2;
-    static constexpr int OFF_O = OFF_Q + 2 * QB;         // [NMT][2][16][SCR]
-    static constexpr int OFF_ML = OFF_O + 2 * RM * SCR * 4;  // [RW][16] (m, l)
-    static constexpr int OFF_U = OFF_ML + RW * 16 * 8;
+    static constexpr int OFF_O = OFF_Q + 2 * QB;         // [NMT][2][WR][SCR]
+    static constexpr int OFF_ML = OFF_O + 2 * RM * SCR * 4;  // [RW][WR] (m, l)
+    static constexpr int OFF_U = OFF_ML + RW * WR * 8;
     static constexpr int OFF_PIECE = OFF_U + (PAGED_MAX_B + 1) * 8;
     static constexpr int OFF_BAR = OFF_PIECE + (RPIECES * static_cast<int>(sizeof(RowPiece)) + 7) / 8 * 8;
     // full[STAGES], empty[STAGES], q_full[2], q_empty[2], piece_full[RPIECES], piece_empty[RPIECES]
@@ -89,18 +93,26 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t w)  // the low two codes
-{
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
-    return h;
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
     uint32_t h;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
     return h;
+}
+
+// The four codes of w, two fp16 pairs.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ float lg2(float x)
@@ -180,12 +192,12 @@ __device__ void join_pieces(const ChunkArgs& a, int f, int i0, int i1, int step,
     }
 }
 
-template <int D, bool FP8, int NMT>
-__global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>::CTAS)
+template <int D, bool FP8, int NQ, int NMT>
+__global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, NQ, NMT>::CTAS)
     chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, ChunkArgs a)
 {
-    using C = RCfg<D, FP8, NMT>;
-    constexpr int KS = D / 16, DT = D / 8, STAGES = C::STAGES, RM = C::RM, RW = C::RW;
+    using C = RCfg<D, FP8, NQ, NMT>;
+    constexpr int KS = D / 16, STAGES = C::STAGES, RM = C::RM, RW = C::RW, WR = C::WR;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* s_o = reinterpret_cast<float*>(smem + C::OFF_O);
@@ -415,191 +427,196 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>:
     RowPiece pc, split[2];
     for (int np = 0; take_piece(np, pc); ++np) {
         const int rows = pc.n * a.g;
-        // Q fragments (rows past the last one: zero), and with FP8 the rows' powers of two
-        uint32_t qa[KS][4];
-        float qs0 = sl2, qs1 = sl2;
+        // Q^T fragments: thread's query row r0 of each n-tile (rows past the last one: zero)
+        uint32_t qb[NQ][KS][2];
+        float qs[NQ][2];  // what turns a raw score of queries 2 cq, 2 cq + 1 into log2 units
+        int pos[NQ][2];   // their positions
         {
             const bool have = warp_wait(&q_full[np & 1], (np / 2) & 1, s_abort);
             const uint8_t* sq = smem + C::OFF_Q + (np & 1) * C::QB;
-            const int ra = mt * 16 + r0, rb = ra + 8;
-            const bool va = have && ra < rows, vb = have && rb < rows;
-            if constexpr (FP8) {
-                // k step 4 h + s of thread cq: columns 64 h + 16 cq + 4 s + {0, 1 | 2, 3}
-                float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const int col = (ks >> 2) * 64 + cq * 16 + (ks & 3) * 4;
-                    const uint2 x = va ? *reinterpret_cast<const uint2*>(sq + (ra * D + col) * 2) : make_uint2(0, 0);
-                    const uint2 y = vb ? *reinterpret_cast<const uint2*>(sq + (rb * D + col) * 2) : make_uint2(0, 0);
-                    qa[ks][0] = x.x;
-                    qa[ks][1] = y.x;
-                    qa[ks][2] = x.y;
-                    qa[ks][3] = y.y;
-                    m0 = fmaxf(m0, fmaxf(fmaxf(fabsf(bf16_lo(x.x)), fabsf(bf16_hi(x.x))), fmaxf(fabsf(bf16_lo(x.y)), fabsf(bf16_hi(x.y)))));
-                    m1 = fmaxf(m1, fmaxf(fmaxf(fabsf(bf16_lo(y.x)), fabsf(bf16_hi(y.x))), fmaxf(fabsf(bf16_lo(y.y)), fabsf(bf16_hi(y.y)))));
+            for (int n = 0; n < NQ; ++n) {
+                const int row = mt * WR + n * 8 + r0;
+                const bool v = have && row < rows;
+                const uint8_t* qr = sq + row * D * 2;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    qs[n][e] = sl2;
+                    pos[n][e] = pc.pos0 + ((mt * WR + n * 8 + 2 * cq + e) >> gs);
                 }
-                m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 1));
-                m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 2));
-                m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
-                m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 2));
-                // largest element to [2^14, 2^15): two factors, as one alone may leave fp32's range
-                const int x0 = m0 > 0.f ? 14 - ilogbf(m0) : 0, x1 = m1 > 0.f ? 14 - ilogbf(m1) : 0;
-                const float fa0 = ldexpf(1.f, x0 / 2), fb0 = ldexpf(1.f, x0 - x0 / 2);
-                const float fa1 = ldexpf(1.f, x1 / 2), fb1 = ldexpf(1.f, x1 - x1 / 2);
-                qs0 = ldexpf(sl2, -x0);
-                qs1 = ldexpf(sl2, -x1);
+                if constexpr (FP8) {
+                    // k step x of thread cq: columns (D / 4) cq + 4 x + {0, 1 | 2, 3}
+                    float m = 0.f;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float fa = (i & 1) ? fa1 : fa0, fb = (i & 1) ? fb1 : fb0;
-                        qa[ks][i] = pack_f16x2(bf16_lo(qa[ks][i]) * fa * fb, bf16_hi(qa[ks][i]) * fa * fb);
+                    for (int x = 0; x < KS; ++x) {
+                        const uint2 y = v ? *reinterpret_cast<const uint2*>(qr + (cq * (D / 4) + 4 * x) * 2) : make_uint2(0, 0);
+                        qb[n][x][0] = y.x;
+                        qb[n][x][1] = y.y;
+                        m = fmaxf(m, fmaxf(fmaxf(fabsf(bf16_lo(y.x)), fabsf(bf16_hi(y.x))), fmaxf(fabsf(bf16_lo(y.y)), fabsf(bf16_hi(y.y)))));
                     }
-                }
-            } else {
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    // largest element to [2^14, 2^15): two factors, as one alone may leave fp32's range
+                    const int ex = m > 0.f ? 14 - ilogbf(m) : 0;
+                    const float fa = ldexpf(1.f, ex / 2), fb = ldexpf(1.f, ex - ex / 2);
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const int col = ks * 16 + 2 * cq;
-                    qa[ks][0] = va ? *reinterpret_cast<const uint32_t*>(sq + (ra * D + col) * 2) : 0u;
-                    qa[ks][1] = vb ? *reinterpret_cast<const uint32_t*>(sq + (rb * D + col) * 2) : 0u;
-                    qa[ks][2] = va ? *reinterpret_cast<const uint32_t*>(sq + (ra * D + col + 8) * 2) : 0u;
-                    qa[ks][3] = vb ? *reinterpret_cast<const uint32_t*>(sq + (rb * D + col + 8) * 2) : 0u;
+                    for (int x = 0; x < KS; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            qb[n][x][e] = pack_f16x2(bf16_lo(qb[n][x][e]) * fa * fb, bf16_hi(qb[n][x][e]) * fa * fb);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) qs[n][e] = ldexpf(sl2, -__shfl_sync(0xffffffffu, ex, (2 * cq + e) * 4));
+                } else {
+#pragma unroll
+                    for (int x = 0; x < KS; ++x) {
+                        qb[n][x][0] = v ? *reinterpret_cast<const uint32_t*>(qr + (x * 16 + 2 * cq) * 2) : 0u;
+                        qb[n][x][1] = v ? *reinterpret_cast<const uint32_t*>(qr + (x * 16 + 2 * cq + 8) * 2) : 0u;
+                    }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_empty[np & 1]);
         }
-        const int pos_a = pc.pos0 + ((mt * 16 + r0) >> gs), pos_b = pc.pos0 + ((mt * 16 + r0 + 8) >> gs);
-        float o[DT][4];
+        const int pos_min = pc.pos0 + ((mt * WR) >> gs);
+        float o[NQ][D / 16][4];  // O^T: 16 columns of V, 8 query rows
+        float m[NQ][2], l[NQ][2];
 #pragma unroll
-        for (int i = 0; i < DT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+        }
 
         for (int t = pc.tb; t < pc.te; ++t, ++it) {
             if ((it & 1) != turn) continue;
             const uint32_t s = it % STAGES;
             if (ready(&full[s], (it / STAGES) & 1, s_abort)) {
                 const uint8_t* kt = smem + s * C::STAGE;
-                const uint8_t* vt = kt + C::TILE;
+                const uint32_t sk = smem_u32(kt), sv = sk + C::TILE;
                 const uint32_t bad = s_bad[s] >> (tok0 / 16) & 3u;  // this warp's groups of 16 keys without a page
                 const int nv = pc.keys - t * RK - tok0;             // keys of this warp's that are in use
-                float sc[4][4];
+                // ---- S^T: 2 m-tiles of 16 keys ----
+                float sc[NQ][2][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) sc[n][i][0] = sc[n][i][1] = sc[n][i][2] = sc[n][i][3] = 0.f;
                 if constexpr (FP8) {
-                    // D = 128: odd keys read their upper 64 codes first, so that two keys' reads fall
-                    // on different banks
-                    const int odd = r0 & 1;
-                    uint4 k4[4][D / 64];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = tok0 + i * 8 + r0;
-                        if constexpr (D == 128) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(kt + swz128(row, odd * 4 + cq));
-                            const uint4 y = *reinterpret_cast<const uint4*>(kt + swz128(row, (odd ^ 1) * 4 + cq));
-                            k4[i][0] = odd ? y : x;
-                            k4[i][D / 64 - 1] = odd ? x : y;
-                        } else {
-                            k4[i][0] = *reinterpret_cast<const uint4*>(kt + swz64(row, cq));
+                    for (int y = 0; y < D / 64; ++y) {  // D = 128: the thread's 32 codes are chunks 2 cq and 2 cq + 1
+                        uint4 ka[2], kb[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int row = tok0 + i * 16 + r0;
+                            ka[i] = *reinterpret_cast<const uint4*>(kt + (D == 128 ? swz128(row, 2 * cq + y) : swz64(row, cq)));
+                            kb[i] = *reinterpret_cast<const uint4*>(kt + (D == 128 ? swz128(row + 8, 2 * cq + y) : swz64(row + 8, cq)));
                         }
-                    }
-#pragma unroll
-                    for (int h = 0; h < D / 64; ++h)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t kw = x == 0 ? k4[i][h].x : x == 1 ? k4[i][h].y : x == 2 ? k4[i][h].z : k4[i][h].w;
-                                mma_f16_16816(sc[i], qa[h * 4 + x], codes_to_f16x2(kw), codes_to_f16x2(kw >> 16));
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t wa = x == 0 ? ka[i].x : x == 1 ? ka[i].y : x == 2 ? ka[i].z : ka[i].w;
+                                const uint32_t wb = x == 0 ? kb[i].x : x == 1 ? kb[i].y : x == 2 ? kb[i].z : kb[i].w;
+                                uint32_t f[4];
+                                codes_to_f16(wa, f[0], f[2]);
+                                codes_to_f16(wb, f[1], f[3]);
+#pragma unroll
+                                for (int n = 0; n < NQ; ++n) mma_f16_16816(sc[n][i], f, qb[n][y * 4 + x][0], qb[n][y * 4 + x][1]);
                             }
+                    }
                 } else {
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        const int dim = ks * 16 + ((mi & 1) << 3);
+                    for (int x = 0; x < KS; ++x) {
+                        const int dim = x * 16 + ((mi >> 1) << 3);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            uint32_t b0, b1, b2, b3;
-                            ldsm_x4(smem_u32(kt) + (dim >> 6) * C::BOX +
-                                        swz128(tok0 + j * 16 + rr + ((mi >> 1) << 3), (dim & 63) >> 3),
-                                    b0, b1, b2, b3);
-                            mma_bf16_16816(sc[2 * j], qa[ks], b0, b1);
-                            mma_bf16_16816(sc[2 * j + 1], qa[ks], b2, b3);
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t f[4];
+                            ldsm_x4(sk + (dim >> 6) * C::BOX + swz128(tok0 + i * 16 + rr + ((mi & 1) << 3), (dim & 63) >> 3),
+                                    f[0], f[1], f[2], f[3]);
+#pragma unroll
+                            for (int n = 0; n < NQ; ++n) mma_bf16_16816(sc[n][i], f, qb[n][x][0], qb[n][x][1]);
                         }
                     }
                 }
                 // ---- scores in log2 units; keys past a row's position (or without a page) -> -inf ----
-                const bool masked = bad || t * RK + tok0 + 31 > pc.pos0 + ((mt * 16) >> gs);
-                float2 lv[4];  // log2 of the values' scales (FP8)
-                float mx0 = -INFINITY, mx1 = -INFINITY;
+                const bool masked = bad || t * RK + tok0 + 31 > pos_min;
+                float ks[2][2], lv[2][2];  // (FP8) scales of keys r0 and r0 + 8 of each m-tile; log2 of the values'
+                if constexpr (FP8) {
+                    const float* scl = reinterpret_cast<const float*>(smem + C::OFF_SC + s * C::SCB) + tok0 + r0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float2 kv = make_float2(1.f, 1.f);
-                    if constexpr (FP8) {
-                        const float* scl = reinterpret_cast<const float*>(smem + C::OFF_SC + s * C::SCB) + tok0 + i * 8 + 2 * cq;
-                        kv = *reinterpret_cast<const float2*>(scl);
-                        const float2 v = *reinterpret_cast<const float2*>(scl + RK);
-                        lv[i] = make_float2(lg2(v.x), lg2(v.y));  // a zero row: -inf, its weight 0
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            ks[i][e] = scl[i * 16 + e * 8];
+                            lv[i][e] = lg2(scl[RK + i * 16 + e * 8]);  // a zero row: -inf, its weight 0
+                            // a scale that stands for no key may be anything, NaN included
+                            if (masked && ((bad >> i & 1u) || i * 16 + e * 8 + r0 >= nv)) lv[i][e] = 0.f;
+                        }
+                }
+                bool up = false;
+                float mx[NQ][2];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    mx[n][0] = mx[n][1] = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float x = sc[n][i][e] * (FP8 ? qs[n][e & 1] * ks[i][e >> 1] : sl2);
+                            if (masked && ((bad >> i & 1u) || t * RK + tok0 + i * 16 + (e >> 1) * 8 + r0 > pos[n][e & 1])) x = -INFINITY;
+                            sc[n][i][e] = x;
+                            // FP8: the sums use the same reference as the weighted values: it may lie below the
+                            // largest score (rows of tiny scale), but by no more than fp32 holds
+                            mx[n][e & 1] = fmaxf(mx[n][e & 1], FP8 ? fmaxf(x + lv[i][e >> 1], x - 100.f) : x);
+                        }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], 4));
+                        mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], 8));
+                        mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], 16));
+                        up |= mx[n][e] > m[n][e];
                     }
-                    sc[i][0] *= qs0 * kv.x;
-                    sc[i][1] *= qs0 * kv.y;
-                    sc[i][2] *= qs1 * kv.x;
-                    sc[i][3] *= qs1 * kv.y;
-                    if (masked) {
-                        const int k = t * RK + tok0 + i * 8 + 2 * cq;
-                        const bool b = bad >> (i >> 1) & 1u;
+                }
+                if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (b || k + (e & 1) > (e < 2 ? pos_a : pos_b)) sc[i][e] = -INFINITY;
-                        if (FP8) {  // such a key's scale may be anything, NaN included
-                            if (b || k >= pc.keys) lv[i].x = 0.f;
-                            if (b || k + 1 >= pc.keys) lv[i].y = 0.f;
+                    for (int n = 0; n < NQ; ++n) {
+                        float al[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float mn = fmaxf(m[n][e], mx[n][e]);
+                            al[e] = m[n][e] == -INFINITY ? 0.f : fast_exp2(m[n][e] - mn);
+                            l[n][e] *= al[e];
+                            m[n][e] = mn;
+                        }
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            o[n][i][0] *= al[0];
+                            o[n][i][1] *= al[1];
+                            o[n][i][2] *= al[0];
+                            o[n][i][3] *= al[1];
                         }
                     }
-                    if constexpr (FP8) {
-                        // the sums use the same reference as the weighted values: it may lie below the largest
-                        // score (rows of tiny scale), but by no more than fp32 holds
-                        mx0 = fmaxf(mx0, fmaxf(fmaxf(sc[i][0] + lv[i].x, sc[i][1] + lv[i].y), fmaxf(sc[i][0], sc[i][1]) - 100.f));
-                        mx1 = fmaxf(mx1, fmaxf(fmaxf(sc[i][2] + lv[i].x, sc[i][3] + lv[i].y), fmaxf(sc[i][2], sc[i][3]) - 100.f));
-                    } else {
-                        mx0 = fmaxf(mx0, fmaxf(sc[i][0], sc[i][1]));
-                        mx1 = fmaxf(mx1, fmaxf(sc[i][2], sc[i][3]));
+                }
+                // ---- P^T ----
+                uint32_t pb[NQ][2][2];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    const float mu[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0], m[n][1] == -INFINITY ? 0.f : m[n][1]};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = sc[n][i][e] - mu[e & 1], y = fast_exp2(x);
+                            l[n][e & 1] += y;
+                            w[e] = FP8 ? fast_exp2(x + lv[i][e >> 1]) : y;
+                        }
+                        pb[n][i][0] = transpose8x8(FP8 ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
+                        pb[n][i][1] = transpose8x8(FP8 ? pack_f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));
                     }
                 }
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-                if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
-                    const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-                    const float al0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - mn0), al1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mn1);
-                    l0 *= al0;
-                    l1 *= al1;
-#pragma unroll
-                    for (int i = 0; i < DT; ++i) {
-                        o[i][0] *= al0;
-                        o[i][1] *= al0;
-                        o[i][2] *= al1;
-                        o[i][3] *= al1;
-                    }
-                    m0 = mn0;
-                    m1 = mn1;
-                }
-                const float mu0 = m0 == -INFINITY ? 0.f : m0, mu1 = m1 == -INFINITY ? 0.f : m1;
-                uint32_t pa[2][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = sc[i][e] - (e < 2 ? mu0 : mu1), y = fast_exp2(x);
-                        if (e < 2) l0 += y;
-                        else l1 += y;
-                        w[e] = FP8 ? fast_exp2(x + ((e & 1) ? lv[i].y : lv[i].x)) : y;
-                    }
-                    pa[i >> 1][2 * (i & 1)] = FP8 ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]);
-                    pa[i >> 1][2 * (i & 1) + 1] = FP8 ? pack_f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]);
-                }
-                // ---- O += P V; rows behind the last key in use may hold anything: zeros instead ----
+                // ---- O^T += V^T P^T; rows behind the last key in use may hold anything: zeros instead ----
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const bool b = bad >> j & 1u;
@@ -610,14 +627,14 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>:
                         z0 = b ? 0u : (v0 < nv ? 0x0000ffffu : 0u) | (v0 + 1 < nv ? 0xffff0000u : 0u);
                         z1 = b ? 0u : (v0 + 8 < nv ? 0x0000ffffu : 0u) | (v0 + 9 < nv ? 0xffff0000u : 0u);
                     }
-                    const int vrow = tok0 + j * 16 + rr + ((mi & 1) << 3);
                     if constexpr (FP8) {
+                        const int vrow = tok0 + j * 16 + rr + ((mi & 1) << 3);
 #pragma unroll
                         for (int dg = 0; dg < D / 32; ++dg) {
                             // keys 0-7 | 8-15 of 16 columns, and of the next 16
                             const int ch = dg * 2 + (mi >> 1);
                             uint32_t v[4];
-                            ldsm_x4_t(smem_u32(vt) + (D == 128 ? swz128(vrow, ch) : swz64(vrow, ch)), v[0], v[1], v[2], v[3]);
+                            ldsm_x4_t(sv + (D == 128 ? swz128(vrow, ch) : swz64(vrow, ch)), v[0], v[1], v[2], v[3]);
                             if (tail) {
                                 v[0] &= z0;
                                 v[2] &= z0;
@@ -625,26 +642,30 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>:
                                 v[3] &= z1;
                             }
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) v[x] = __byte_perm(v[x], 0u, 0x3120);  // even columns' pair | odd columns'
-                            mma_f16_16816(o[4 * dg], pa[j], codes_to_f16x2(v[0]), codes_to_f16x2(v[1]));
-                            mma_f16_16816(o[4 * dg + 1], pa[j], codes_to_f16x2(v[0] >> 16), codes_to_f16x2(v[1] >> 16));
-                            mma_f16_16816(o[4 * dg + 2], pa[j], codes_to_f16x2(v[2]), codes_to_f16x2(v[3]));
-                            mma_f16_16816(o[4 * dg + 3], pa[j], codes_to_f16x2(v[2] >> 16), codes_to_f16x2(v[3] >> 16));
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t f[4];
+                                // even columns' pair of keys | odd columns'
+                                codes_to_f16(__byte_perm(v[2 * h], 0u, 0x3120), f[0], f[1]);
+                                codes_to_f16(__byte_perm(v[2 * h + 1], 0u, 0x3120), f[2], f[3]);
+#pragma unroll
+                                for (int n = 0; n < NQ; ++n) mma_f16_16816(o[n][2 * dg + h], f, pb[n][j][0], pb[n][j][1]);
+                            }
                         }
                     } else {
+                        const int vrow = tok0 + j * 16 + rr + ((mi >> 1) << 3);
 #pragma unroll
                         for (int dp = 0; dp < D / 16; ++dp) {
-                            const int dim = dp * 16 + ((mi >> 1) << 3);
-                            uint32_t v0, v1, v2, v3;
-                            ldsm_x4_t(smem_u32(vt) + (dim >> 6) * C::BOX + swz128(vrow, (dim & 63) >> 3), v0, v1, v2, v3);
+                            const int dim = dp * 16 + ((mi & 1) << 3);
+                            uint32_t f[4];
+                            ldsm_x4_t(sv + (dim >> 6) * C::BOX + swz128(vrow, (dim & 63) >> 3), f[0], f[1], f[2], f[3]);
                             if (tail) {
-                                v0 &= z0;
-                                v2 &= z0;
-                                v1 &= z1;
-                                v3 &= z1;
+                                f[0] &= z0;
+                                f[1] &= z0;
+                                f[2] &= z1;
+                                f[3] &= z1;
                             }
-                            mma_bf16_16816(o[2 * dp], pa[j], v0, v1);
-                            mma_bf16_16816(o[2 * dp + 1], pa[j], v2, v3);
+#pragma unroll
+                            for (int n = 0; n < NQ; ++n) mma_bf16_16816(o[n][dp], f, pb[n][j][0], pb[n][j][1]);
                         }
                     }
                 }
@@ -654,74 +675,71 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>:
         }
 
         // ---- join the four warps: each row's common maximum, then sums over scratch memory ----
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-        if (cq == 0) {
-            s_ml[warp * 16 + r0] = make_float2(m0, l0);
-            s_ml[warp * 16 + r0 + 8] = make_float2(m1, l1);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+                if (r0 == 0) s_ml[warp * WR + n * 8 + 2 * cq + e] = make_float2(m[n][e], l[n][e]);
+            }
+        named_bar_sync(1, RW * 32);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float2* ml = s_ml + mt * 4 * WR + n * 8 + 2 * cq + e;
+                float M = -INFINITY, L = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) M = fmaxf(M, ml[j * WR].x);
+                const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) L += fast_exp2(ml[j * WR].x - mu) * ml[j * WR].y;
+                const float w = fast_exp2(m[n][e] - mu);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    o[n][i][e] *= w;
+                    o[n][i][2 + e] *= w;
+                }
+                m[n][e] = M;
+                l[n][e] = L;
+            }
+        // (query row, first column, and the step to the second one) of o[n][i][e] and o[n][i][2 + e]
+        constexpr int CS = FP8 ? 1 : 8;
+        float* so = s_o + (mt * 2 + (sub & 1)) * WR * C::SCR + 2 * cq * C::SCR + (FP8 ? 2 * r0 : r0);
+        if (sub >= 2) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) so[(n * 8 + (e & 1)) * C::SCR + i * 16 + (e >> 1) * CS] = o[n][i][e];
         }
         named_bar_sync(1, RW * 32);
-        float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
+        if (sub < 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            M0 = fmaxf(M0, s_ml[(mt * 4 + j) * 16 + r0].x);
-            M1 = fmaxf(M1, s_ml[(mt * 4 + j) * 16 + r0 + 8].x);
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) so[(n * 8 + (e & 1)) * C::SCR + i * 16 + (e >> 1) * CS] += o[n][i][e];
         }
-        const float mu0 = M0 == -INFINITY ? 0.f : M0, mu1 = M1 == -INFINITY ? 0.f : M1;
+        if (sub == 0 && r0 == 0) {  // (every warp has read the sums)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 x = s_ml[(mt * 4 + j) * 16 + r0], y = s_ml[(mt * 4 + j) * 16 + r0 + 8];
-            L0 += fast_exp2(x.x - mu0) * x.y;
-            L1 += fast_exp2(y.x - mu1) * y.y;
-        }
-        const float w0 = fast_exp2(m0 - mu0), w1 = fast_exp2(m1 - mu1);
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int i = 0; i < DT; ++i) {
-            o[i][0] *= w0;
-            o[i][1] *= w0;
-            o[i][2] *= w1;
-            o[i][3] *= w1;
-        }
-        // column of o[i][e]: FP8: 16 (i / 2) + 4 cq + 2 (e & 1) + (i & 1); bf16: 8 i + 2 cq + (e & 1)
-        auto col = [&](int i, int e) { return FP8 ? (i >> 1) * 16 + 4 * cq + 2 * e + (i & 1) : i * 8 + 2 * cq + e; };
-        auto spill = [&](float* so) {
-#pragma unroll
-            for (int i = 0; i < DT; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    so[r0 * C::SCR + col(i, e)] = o[i][e];
-                    so[(r0 + 8) * C::SCR + col(i, e)] = o[i][2 + e];
-                }
-        };
-        auto fill = [&](const float* so) {
-#pragma unroll
-            for (int i = 0; i < DT; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    o[i][e] += so[r0 * C::SCR + col(i, e)];
-                    o[i][2 + e] += so[(r0 + 8) * C::SCR + col(i, e)];
-                }
-        };
-        float* so = s_o + (mt * 2 + (sub & 1)) * 16 * C::SCR;
-        if (sub >= 2) spill(so);
-        named_bar_sync(1, RW * 32);
-        if (sub < 2) fill(so);
-        if (sub < 2) spill(so);
-        if (sub == 0 && cq == 0) {
-            s_ml[warp * 16 + r0] = make_float2(M0, L0);  // (every warp has read the sums)
-            s_ml[warp * 16 + r0 + 8] = make_float2(M1, L1);
+                for (int e = 0; e < 2; ++e) s_ml[warp * WR + n * 8 + 2 * cq + e] = make_float2(m[n][e], l[n][e]);
         }
         named_bar_sync(1, RW * 32);
         // ---- the rows: finished, or a partial ----
         const long long slot = static_cast<long long>(2 * c + (c == pc.first ? 1 : 0)) * RM;
         for (int idx = threadIdx.x; idx < rows * (D / 4); idx += RW * 32) {
             const int r = idx / (D / 4), q4 = idx - r * (D / 4);
-            const float* sr = s_o + ((r >> 4) * 32 + (r & 15)) * C::SCR + 4 * q4;
-            const float4 x = *reinterpret_cast<const float4*>(sr), y = *reinterpret_cast<const float4*>(sr + 16 * C::SCR);
+            const float* sr = s_o + ((r / WR) * 2 * WR + r % WR) * C::SCR + 4 * q4;
+            const float4 x = *reinterpret_cast<const float4*>(sr), y = *reinterpret_cast<const float4*>(sr + WR * C::SCR);
             const float4 v = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-            const float2 ml = s_ml[(r >> 4) * 64 + (r & 15)];
+            const float2 ml = s_ml[(r / WR) * 4 * WR + r % WR];
             if (pc.count == 1) {
                 const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
                 const long long row = static_cast<long long>(pc.t0 + (r >> gs)) * a.H + static_cast<long long>(pc.kvh) * a.g + (r & (a.g - 1));
@@ -784,31 +802,33 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NMT>::THREADS, RCfg<D, FP8, NMT>:
     }
 }
 
-template <int D, bool FP8, int NMT>
+template <int D, bool FP8, int NQ, int NMT>
 cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
                          cudaStream_t stream)
 {
-    using C = RCfg<D, FP8, NMT>;
+    using C = RCfg<D, FP8, NQ, NMT>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(chunk_rows_kernel<D, FP8, NMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        e = cudaFuncSetAttribute(chunk_rows_kernel<D, FP8, NQ, NMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
     int grid = num_sms * C::CTAS;
     if (grid > CHUNK_MAX_SLOTS) grid = CHUNK_MAX_SLOTS;
-    return launch_pdl(chunk_rows_kernel<D, FP8, NMT>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tm_k, tm_v, a);
+    return launch_pdl(chunk_rows_kernel<D, FP8, NQ, NMT>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tm_k, tm_v, a);
 }
 
 template <int D, bool FP8>
 cudaError_t launch_rows(const ChunkArgs& a, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
                         cudaStream_t stream)
 {
-    return a.max_q * a.g <= 16 ? launch_typed<D, FP8, 1>(a, tm_k, tm_v, num_sms, stream)
-                               : launch_typed<D, FP8, 2>(a, tm_k, tm_v, num_sms, stream);
+    const int rows = a.max_q * a.g;
+    return rows <= 8    ? launch_typed<D, FP8, 1, 1>(a, tm_k, tm_v, num_sms, stream)
+           : rows <= 16 ? launch_typed<D, FP8, 2, 1>(a, tm_k, tm_v, num_sms, stream)
+                        : launch_typed<D, FP8, 2, 2>(a, tm_k, tm_v, num_sms, stream);
 }
 
 }  // namespace
