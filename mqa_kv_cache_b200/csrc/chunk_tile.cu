@@ -32,24 +32,6 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: the maximum moves only when it grows by more than 2^8
 
-// Degree-4 polynomial for 2^f on [-1/2, 1/2], minimax in relative error (2.7e-6 in fp32
-// Horner form), produced by fit_exp2_poly.py's remez(4): the sums enter an fp32 output
-// (lse), which the degree-3 one's 7.5e-5 would show in.
-__device__ __forceinline__ float2 exp2_poly2(float2 x)
-{
-    x.x = fmaxf(x.x, -125.f);
-    x.y = fmaxf(x.y, -125.f);
-    const float2 t = __fadd2_rn(x, make_float2(kShifter, kShifter));
-    const float2 n = __fadd2_rn(t, make_float2(-kShifter, -kShifter));
-    const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
-    float2 p = __ffma2_rn(make_float2(0.009570102f, 0.009570102f), f, make_float2(0.05591786f, 0.05591786f));
-    p = __ffma2_rn(p, f, make_float2(0.24024744f, 0.24024744f));
-    p = __ffma2_rn(p, f, make_float2(0.6931218f, 0.6931218f));
-    p = __ffma2_rn(p, f, make_float2(0.9999993f, 0.9999993f));
-    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
-}
-
 // A stretch of one unit's key tiles, as warp 11 hands it to the others (rows = 0: no more).
 struct Piece {
     int b, kvh;
@@ -118,6 +100,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
+// warp_wait with a first look that asks for the phase alone.
+__device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity, volatile int* abort_flag)
+{
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || warp_wait(bar, parity, abort_flag);
+}
+
 // The MMA warp runs its loop with all lanes, so that the descriptors stay in uniform
 // registers (under a one-lane branch each operand of each MMA is moved there first, about
 // 100 cycles per instruction); only these instructions are for the elected lane.
@@ -155,10 +143,12 @@ __device__ __forceinline__ void commit_to(uint32_t elect, uint64_t* bar)
         : "memory");
 }
 
-// One row's 128 scores (log2 units after sl2) -> weights to TMEM over the scores; returns their sum.
-// MASKED tiles take every exponential from the hardware unit, where 2^-inf is exactly 0;
-// otherwise a quarter go through the polynomial on the FMA pipe.
-template <bool FP8, bool MASKED>
+// One row's 128 scores -> weights 2^(s sl2 - mu) to TMEM over the scores; returns their sum.
+// Every exponential goes through the hardware unit, where 2^-inf is exactly 0.  It is not
+// what bounds the softmax (without any exponential the kernel takes as long): moving a
+// quarter of them to an FMA polynomial cost 10% by its instructions, and a second body
+// for tiles without a mask another 4% by its size.
+template <bool FP8>
 __device__ __forceinline__ float row_weights(const uint32_t (&sv)[4][32], float sl2, float mu, uint32_t s_addr,
                                              const float* vs)
 {
@@ -176,13 +166,7 @@ __device__ __forceinline__ float row_weights(const uint32_t (&sv)[4][32], float 
         for (int i = 0; i < 16; ++i) {
             const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[c][2 * i]), __uint_as_float(sv[c][2 * i + 1])),
                                         sc2, nmu);
-            float2 pr;
-            if (!MASKED && (i & 3) == 0) {
-                pr = exp2_poly2(x);
-            } else {
-                pr.x = fast_exp2(x.x);
-                pr.y = fast_exp2(x.y);
-            }
+            float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
             acc[i & 3] = __fadd2_rn(acc[i & 3], pr);
             if constexpr (FP8) pr = __fmul2_rn(pr, (i & 1) ? make_float2(v4[i / 2].z, v4[i / 2].w) : make_float2(v4[i / 2].x, v4[i / 2].y));
             pk[i] = pack_bf16x2(pr.x, pr.y);
@@ -417,11 +401,11 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             uint32_t pv0 = 0, pv1 = 0;        // P V products issued to each buffer
             int np = 0;
             // scores of Q tile q in buffer t; the weights in its columns have been used by then
-            auto scores = [&](int t, int q, uint32_t x) {
+            auto scores = [&](int t, int q, uint32_t x, bool landed = false) {
                 const uint32_t slot = x % NS;
-                ok = ok && warp_wait(&kv_full[slot], (x / NS) & 1, s_abort);
+                ok = ok && (landed || ready(&kv_full[slot], (x / NS) & 1, s_abort));
                 const uint32_t pv = t ? pv1 : pv0;
-                if (ok && pv) ok = warp_wait(&pv_done[t], (pv - 1) & 1, s_abort);
+                if (ok && pv) ok = ready(&pv_done[t], (pv - 1) & 1, s_abort);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t d = tmem + t * CH_KEYS, qa = sq + q * C::TILE, ka = skv + slot * C::TILE;
@@ -433,10 +417,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 commit_to(el, &s_full[t]);
                 if (el) mbar_arrive(&s_full[t]);
             };
-            auto values = [&](int t, bool acc, uint32_t x) {
+            auto values = [&](int t, bool acc, uint32_t x, bool landed = false) {
                 const uint32_t slot = x % NS;
-                ok = ok && warp_wait(&kv_full[slot], (x / NS) & 1, s_abort);
-                if (ok) ok = warp_wait(&p_full[t], (t ? pv1 : pv0) & 1, s_abort);
+                ok = ok && (landed || ready(&kv_full[slot], (x / NS) & 1, s_abort));
+                if (ok) ok = ready(&p_full[t], (t ? pv1 : pv0) & 1, s_abort);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t va = skv + slot * C::TILE;
@@ -451,14 +435,14 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             Piece u;
             while (ok && take(np, u)) {
                 const int tb = u.tb, te = u.te;
-                ok = warp_wait(q_full, np & 1, s_abort);
+                ok = ready(q_full, np & 1, s_abort);
                 ++np;
                 if (!ok) break;
                 const int n = te - tb;
                 if (u.cost == 2) {
                     const int n0 = min(te, u.tiles0) - tb;  // tiles of Q tile 0 (it may see none of these)
                     if (n0 > 0) scores(0, 0, x0);
-                    scores(1, 1, x0);
+                    scores(1, 1, x0, n0 > 0);
                     if (ok) commit_to(el, &kv_empty[x0 % NS]);
                     if (ok && n == 1) commit_to(el, q_empty);
                     // each Q tile's P V, then at once its next scores
@@ -466,10 +450,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                         const uint32_t xv = x0 + 2 * k + 1, xk = xv + 1;
                         if (k < n0) values(0, k > 0, xv);
                         if (k + 1 < n0) scores(0, 0, xk);
-                        values(1, k > 0, xv);
+                        values(1, k > 0, xv, k < n0);
                         if (ok) commit_to(el, &kv_empty[xv % NS]);
                         if (k + 1 < n) {
-                            scores(1, 1, xk);
+                            scores(1, 1, xk, k + 1 < n0);
                             if (ok) commit_to(el, &kv_empty[xk % NS]);
                             if (ok && k + 2 == n) commit_to(el, q_empty);
                         }
@@ -527,14 +511,14 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             for (int k = 0; k < n_my; ++k, ++cnt) {
                 const int j = pair ? tb + k : tb + 2 * k + t;
                 const uint32_t it = it0 + (j - tb);
-                if (!warp_wait(&s_full[t], cnt & 1, s_abort)) continue;
+                if (!ready(&s_full[t], cnt & 1, s_abort)) continue;
                 tc_fence_after();
                 const int nv = min(u.keys - j * CH_KEYS, CH_KEYS);
                 if (!FP8 && nv < CH_KEYS) {
                     // rows of V behind the last key in use were not loaded, or hold what nobody may see:
                     // zeros, so that 0 * garbage cannot reach a sum (the P V waits for this warp)
                     const uint32_t xv = 2 * it + 1;
-                    if (!warp_wait(&kv_full[xv % NS], (xv / NS) & 1, s_abort)) continue;
+                    if (!ready(&kv_full[xv % NS], (xv / NS) & 1, s_abort)) continue;
                     if (r >= nv) {
                         uint8_t* v = smem + C::OFF_KV + (xv % NS) * C::TILE + r * 128;
 #pragma unroll
@@ -602,8 +586,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     }
                     m_run = m_new;
                     const float mu = m_run == -INFINITY ? 0.f : m_run;
-                    l_run += masked ? row_weights<FP8, true>(sv, sl2, mu, s_addr, ks + CH_KEYS)
-                                    : row_weights<FP8, false>(sv, sl2, mu, s_addr, ks + CH_KEYS);
+                    l_run += row_weights<FP8>(sv, sl2, mu, s_addr, ks + CH_KEYS);
                     tmem_wait_st();
                 }
                 tc_fence_before();
@@ -611,7 +594,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 if (lane == 0) mbar_arrive(&p_full[t]);
             }
             it0 += te - tb;
-            const bool ok = n_my == 0 || warp_wait(&pv_done[t], (cnt - 1) & 1, s_abort);
+            const bool ok = n_my == 0 || ready(&pv_done[t], (cnt - 1) & 1, s_abort);
             tc_fence_after();
             // ---- the piece's rows: finished, or a partial for the merge ----
             const long long orow = (static_cast<long long>(u.tok0) + (row >> gs)) * a.H +
@@ -626,7 +609,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&joined[0]);
-                warp_wait(&joined[0], joins & 1, s_abort);
+                ready(&joined[0], joins & 1, s_abort);
                 tc_fence_after();
                 const float2 o = s_ml[(t ^ 1) * 128 + r];
                 m = fmaxf(m_run, o.x);
@@ -687,7 +670,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             if (!pair) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&joined[1]);
-                warp_wait(&joined[1], joins & 1, s_abort);
+                ready(&joined[1], joins & 1, s_abort);
                 ++joins;
             }
         }
@@ -706,8 +689,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     const uint32_t it = x / 2;
                     for (int kv = 0; kv < 2; ++kv, ++x) {
                         const uint32_t ls = x % (LS > 0 ? LS : 1), slot = x % NS;
-                        ok = warp_wait(&land_full[ls], (x / (LS > 0 ? LS : 1)) & 1, s_abort);
-                        if (ok && x >= NS) ok = warp_wait(&kv_empty[slot], (x / NS - 1) & 1, s_abort);
+                        ok = ready(&land_full[ls], (x / (LS > 0 ? LS : 1)) & 1, s_abort);
+                        if (ok && x >= NS) ok = ready(&kv_empty[slot], (x / NS - 1) & 1, s_abort);
                         if (!ok) break;
                         const uint32_t bad = s_bad[it % C::RING];
                         const bool partial = nv < CH_KEYS || bad != 0;
