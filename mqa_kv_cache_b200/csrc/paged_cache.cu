@@ -9,6 +9,8 @@
 // Memory-bound, and latency-bound for a decode step's few rows: a row's data is
 // requested before its place is known, and the batch's offsets and lengths come in
 // one round trip through shared memory.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace kvattn {
@@ -24,54 +26,92 @@ __device__ __forceinline__ uint32_t codes_x2(float lo, float hi)
     return r;
 }
 
-// One row's scale (absmax over the CPR lanes holding it) and this lane's eight codes.
-template <int CPR>
-__device__ __forceinline__ uint2 quantise_row(const float (&x)[8], float& s)
+// One row's scale (absmax over the CPR lanes holding it) and this lane's E codes, four a word.
+// Division by Markstein's method (P. Markstein, IBM J. Res. Dev. 34, 1990): r = RN(1 / s),
+// q = RN(x r), and q + r (x - q s) with both products fused, whose error before its rounding is
+// under 2^-23 ulp.  It can differ from RN(x / s) only where x / s lies that close to the middle of
+// two floats, and the code only where that middle is also next to a border between codes, a
+// number of five bits: for which s has to be within 2 ulp of a multiple of 2^-3 of its binade.
+// tests/test_paged_quant_rule.py enumerates those: the code is the divided quotient's in all.
+template <int CPR, int E>
+__device__ __forceinline__ void quantise_row(const float (&x)[E], float& s, uint32_t (&c)[E / 4])
 {
     float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[i]));
+    for (int i = 0; i < E; i += 2) a = fmax3(a, fabsf(x[i]), fabsf(x[i + 1]));
 #pragma unroll
     for (int o = CPR / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     s = __fdiv_rn(a, 448.f);
-    if (s == 0.f) return make_uint2(0u, 0u);
-    uint32_t c[4];
+    if (s > 0x1p-100f && s < 0x1p100f) {
+        const float r = __frcp_rn(s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = codes_x2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s));
-    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-}
-
-__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8])
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < E / 4; ++i) {
+            uint32_t h[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
+            for (int k = 0; k < 2; ++k) {
+                const float2 y = make_float2(x[4 * i + 2 * k], x[4 * i + 2 * k + 1]);
+                const float2 q = __fmul2_rn(y, make_float2(r, r));
+                const float2 e = __ffma2_rn(q, make_float2(-s, -s), y);
+                const float2 z = __ffma2_rn(e, make_float2(r, r), q);
+                h[k] = codes_x2(z.x, z.y);
+            }
+            c[i] = h[0] | (h[1] << 16);
+        }
+    } else {  // a zero row, or a scale whose reciprocal leaves the normal range
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            c[i] = 0u;
+            if (s != 0.f)
+                c[i] = codes_x2(__fdiv_rn(x[4 * i], s), __fdiv_rn(x[4 * i + 1], s)) |
+                       (codes_x2(__fdiv_rn(x[4 * i + 2], s), __fdiv_rn(x[4 * i + 3], s)) << 16);
+        }
     }
 }
 
-// CPR = d / 8 lanes hold one (token, head) row of K and the same row of V, eight
-// elements each.
-template <int CPR, bool FP8>
+// The elements of N 16-byte pieces.
+template <int N>
+__device__ __forceinline__ void unpack(const uint4 (&v)[N], float (&x)[8 * N])
+{
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[8 * k + 2 * i] = bf16_lo(w[i]);
+            x[8 * k + 2 * i + 1] = bf16_hi(w[i]);
+        }
+    }
+}
+
+// CPR = D / E lanes take one token's rows of K and V for HB KV heads, E elements of each row a
+// lane: its place and its cos / sin entries are looked up once for all of them, and the
+// rows are requested before either is known.
+template <int D, int E, int HB, bool FP8>
 __global__ void __launch_bounds__(AP_THREADS) paged_append_kernel(PagedAppendArgs a)
 {
-    constexpr int D = CPR * 8;
+    constexpr int CPR = D / E, N = E / 8;
     __shared__ int s_cu[PAGED_MAX_B + 1], s_len[PAGED_MAX_B];
     pdl_wait();
     pdl_trigger();
     const PagedBatch& p = a.p;
     const int ch = threadIdx.x % CPR;
-    const long long rows = static_cast<long long>(p.n_tokens) * a.Hk;
-    const long long step = static_cast<long long>(gridDim.x) * (AP_THREADS / CPR);
-    long long row = static_cast<long long>(blockIdx.x) * (AP_THREADS / CPR) + threadIdx.x / CPR;
-    uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-    auto fetch = [&](long long r) {
-        const int t = static_cast<int>(r / a.Hk), h = static_cast<int>(r - static_cast<long long>(t) * a.Hk);
-        kx = __ldg(reinterpret_cast<const uint4*>(a.k_new + t * a.k_st + h * D) + ch);
-        vx = __ldg(reinterpret_cast<const uint4*>(a.v_new + t * a.v_st + h * D) + ch);
-    };
-    if (row < rows) fetch(row);
+    const int groups = (a.Hk + HB - 1) / HB;
+    const long long item = static_cast<long long>(blockIdx.x) * (AP_THREADS / CPR) + threadIdx.x / CPR;
+    const bool have = item < static_cast<long long>(p.n_tokens) * groups;
+    const int t = have ? static_cast<int>(item / groups) : -1;
+    const int h0 = have ? static_cast<int>(item - static_cast<long long>(t) * groups) * HB : 0;
+    uint4 kx[HB][N], vx[HB][N];
+#pragma unroll
+    for (int i = 0; i < HB; ++i) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            kx[i][k] = vx[i][k] = make_uint4(0, 0, 0, 0);
+            if (have && h0 + i < a.Hk) {
+                kx[i][k] = __ldg(reinterpret_cast<const uint4*>(a.k_new + t * a.k_st + (h0 + i) * D) + ch * N + k);
+                vx[i][k] = __ldg(reinterpret_cast<const uint4*>(a.v_new + t * a.v_st + (h0 + i) * D) + ch * N + k);
+            }
+        }
+    }
     for (int b = threadIdx.x; b <= p.B; b += AP_THREADS) {
         s_cu[b] = p.cu[b];
         if (b < p.B) s_len[b] = p.seq_lens[b];
@@ -80,88 +120,97 @@ __global__ void __launch_bounds__(AP_THREADS) paged_append_kernel(PagedAppendArg
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < p.B; b += AP_THREADS)
             if (paged_seq(p, s_cu[b], s_cu[b + 1], s_len[b]).bad) report_status(p.dev_status, KVATTN_STATUS_BAD_LENGTH);
-    // every lane of a warp takes the same number of turns, for the shuffles
-    for (long long r0 = row - threadIdx.x % 32 / CPR; r0 < rows; r0 += step, row += step) {
-        const uint4 kr = kx, vr = vx;
-        if (row + step < rows) fetch(row + step);
-        const bool have = row < rows;
-        const int t = have ? static_cast<int>(row / a.Hk) : -1;
-        const int h = have ? static_cast<int>(row - static_cast<long long>(t) * a.Hk) : 0;
-        // the sequence of token t: the last b with cu[b] <= t
-        int lo = 0, hi = p.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_cu[mid] <= t) lo = mid;
-            else hi = mid - 1;
-        }
-        const PagedSeq s = paged_seq(p, s_cu[lo], s_cu[lo + 1], s_len[lo]);
-        const bool mine = have && t >= s.t0 && t < s.t0 + s.n;  // not a token behind the last sequence
-        const int pos = s.len - s.n + (t - s.t0);
-        bool go = mine && pos >= 0 && pos < a.max_pos;
-        if (mine && !go && ch == 0) report_status(p.dev_status, KVATTN_STATUS_BAD_POSITION);
-        int page = 0;
-        if (go) {
-            page = p.page_table[static_cast<long long>(lo) * p.max_pages + (pos >> p.page_shift)];
-            if (page < 0 || page >= p.n_pages) {
-                go = false;
-                if (ch == 0) report_status(p.dev_status, KVATTN_STATUS_BAD_INDEX);
-            }
-        }
-        float kf[8];
-        {
-            const long long cs = static_cast<long long>(go ? pos : 0) * (D / 2);
-            float x[8];
-            unpack8(kr, x);
-            if (a.pair_style == 0) {
-                const float4 c = *reinterpret_cast<const float4*>(a.cos_tab + cs + ch * 4);
-                const float4 n = *reinterpret_cast<const float4*>(a.sin_tab + cs + ch * 4);
-                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {n.x, n.y, n.z, n.w};
+    // the sequence of token t: the last b with cu[b] <= t
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_cu[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    const PagedSeq s = paged_seq(p, s_cu[lo], s_cu[lo + 1], s_len[lo]);
+    const bool mine = have && t >= s.t0 && t < s.t0 + s.n;  // not a token behind the last sequence
+    const int pos = s.len - s.n + (t - s.t0);
+    bool go = mine && pos >= 0 && pos < a.max_pos;
+    if (mine && !go && ch == 0) report_status(p.dev_status, KVATTN_STATUS_BAD_POSITION);
+    int page = 0;
+    if (go) page = p.page_table[static_cast<long long>(lo) * p.max_pages + (pos >> p.page_shift)];
+    // cos and sin of this lane's elements: its E / 2 pairs (2i, 2i + 1), or the E of its half
+    float cc[E], ss[E];
+    const bool first = ch < CPR / 2;  // half-split pairs: the lower half
+    {
+        const long long cs = static_cast<long long>(go ? pos : 0) * (D / 2) +
+                             (a.pair_style == 0 ? ch * (E / 2) : (first ? ch : ch - CPR / 2) * E);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 y = rope_pair(x[2 * i], x[2 * i + 1], cc[i], ss[i]);
-                    kf[2 * i] = y.x;
-                    kf[2 * i + 1] = y.y;
-                }
-            } else {
-                // this lane's eight elements pair with those of the lane d/2 further on (or back)
-                uint4 o;
-                o.x = __shfl_xor_sync(0xffffffffu, kr.x, CPR / 2);
-                o.y = __shfl_xor_sync(0xffffffffu, kr.y, CPR / 2);
-                o.z = __shfl_xor_sync(0xffffffffu, kr.z, CPR / 2);
-                o.w = __shfl_xor_sync(0xffffffffu, kr.w, CPR / 2);
-                float y[8];
-                unpack8(o, y);
-                const bool first = ch < CPR / 2;
-                const int ci = (first ? ch : ch - CPR / 2) * 8;
-                const float4 c0 = *reinterpret_cast<const float4*>(a.cos_tab + cs + ci);
-                const float4 c1 = *reinterpret_cast<const float4*>(a.cos_tab + cs + ci + 4);
-                const float4 n0 = *reinterpret_cast<const float4*>(a.sin_tab + cs + ci);
-                const float4 n1 = *reinterpret_cast<const float4*>(a.sin_tab + cs + ci + 4);
-                const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-                const float ss[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    kf[i] = first ? rope_pair(x[i], y[i], cc[i], ss[i]).x : rope_pair(y[i], x[i], cc[i], ss[i]).y;
+        for (int i = 0; i < E; i += 4) {
+            float4 c = make_float4(0.f, 0.f, 0.f, 0.f), n = c;
+            if (i < E / 2 || a.pair_style != 0) {
+                c = *reinterpret_cast<const float4*>(a.cos_tab + cs + i);
+                n = *reinterpret_cast<const float4*>(a.sin_tab + cs + i);
             }
+            cc[i] = c.x, cc[i + 1] = c.y, cc[i + 2] = c.z, cc[i + 3] = c.w;
+            ss[i] = n.x, ss[i + 1] = n.y, ss[i + 2] = n.z, ss[i + 3] = n.w;
         }
-        const long long dst = ((static_cast<long long>(page) * a.Hk + h) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
+    }
+    if (go && (page < 0 || page >= p.n_pages)) {
+        go = false;
+        if (ch == 0) report_status(p.dev_status, KVATTN_STATUS_BAD_INDEX);
+    }
+#pragma unroll
+    for (int j = 0; j < HB; ++j) {
+        float kf[E], x[E];
+        unpack(kx[j], x);
+        if (a.pair_style == 0) {
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                const float2 y = rope_pair(x[2 * i], x[2 * i + 1], cc[i], ss[i]);
+                kf[2 * i] = y.x;
+                kf[2 * i + 1] = y.y;
+            }
+        } else {
+            // this lane's elements pair with those of the lane d/2 further on (or back)
+            uint4 o[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                o[k].x = __shfl_xor_sync(0xffffffffu, kx[j][k].x, CPR / 2);
+                o[k].y = __shfl_xor_sync(0xffffffffu, kx[j][k].y, CPR / 2);
+                o[k].z = __shfl_xor_sync(0xffffffffu, kx[j][k].z, CPR / 2);
+                o[k].w = __shfl_xor_sync(0xffffffffu, kx[j][k].w, CPR / 2);
+            }
+            float y[E];
+            unpack(o, y);
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                kf[i] = first ? rope_pair(x[i], y[i], cc[i], ss[i]).x : rope_pair(y[i], x[i], cc[i], ss[i]).y;
+        }
+        const bool put = go && h0 + j < a.Hk;
+        const long long dst =
+            ((static_cast<long long>(page) * a.Hk + h0 + j) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
         if constexpr (FP8) {
-            float vf[8], ks, vs;
-            unpack8(vr, vf);
-            const uint2 kc = quantise_row<CPR>(kf, ks), vc = quantise_row<CPR>(vf, vs);
-            if (go) {
-                reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k_pages) + dst * D)[ch] = kc;
-                reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_pages) + dst * D)[ch] = vc;
+            using Codes = typename std::conditional<E == 16, uint4, uint2>::type;
+            float vf[E], ks, vs;
+            union {
+                uint32_t w[E / 4];
+                Codes v;
+            } kc, vc;
+            unpack(vx[j], vf);
+            quantise_row<CPR>(kf, ks, kc.w);
+            quantise_row<CPR>(vf, vs, vc.w);
+            if (put) {
+                reinterpret_cast<Codes*>(static_cast<uint8_t*>(a.k_pages) + dst * D)[ch] = kc.v;
+                reinterpret_cast<Codes*>(static_cast<uint8_t*>(a.v_pages) + dst * D)[ch] = vc.v;
                 if (ch == 0) {
                     a.k_scales[dst] = ks;
                     a.v_scales[dst] = vs;
                 }
             }
-        } else if (go) {
-            reinterpret_cast<uint4*>(static_cast<kvattn_bf16*>(a.k_pages) + dst * D)[ch] =
-                make_uint4(pack_bf16x2(kf[0], kf[1]), pack_bf16x2(kf[2], kf[3]), pack_bf16x2(kf[4], kf[5]),
-                           pack_bf16x2(kf[6], kf[7]));
-            reinterpret_cast<uint4*>(static_cast<kvattn_bf16*>(a.v_pages) + dst * D)[ch] = vr;
+        } else if (put) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                reinterpret_cast<uint4*>(static_cast<kvattn_bf16*>(a.k_pages) + dst * D)[ch * N + k] =
+                    make_uint4(pack_bf16x2(kf[8 * k], kf[8 * k + 1]), pack_bf16x2(kf[8 * k + 2], kf[8 * k + 3]),
+                               pack_bf16x2(kf[8 * k + 4], kf[8 * k + 5]), pack_bf16x2(kf[8 * k + 6], kf[8 * k + 7]));
+                reinterpret_cast<uint4*>(static_cast<kvattn_bf16*>(a.v_pages) + dst * D)[ch * N + k] = vx[j][k];
+            }
         }
     }
 }
@@ -215,15 +264,23 @@ __global__ void __launch_bounds__(RD_THREADS) paged_read_kernel(PagedReadArgs a)
 
 }  // namespace
 
+template <int E, int HB, bool FP8>
+cudaError_t launch_append(const PagedAppendArgs& a, cudaStream_t stream)
+{
+    const int per_block = AP_THREADS / (a.d / E);
+    const long long blocks = (static_cast<long long>(a.p.n_tokens) * ((a.Hk + HB - 1) / HB) + per_block - 1) / per_block;
+    return launch_pdl(a.d == 128 ? paged_append_kernel<128, E, HB, FP8> : paged_append_kernel<64, E, HB, FP8>,
+                      dim3(static_cast<unsigned>(blocks)), dim3(AP_THREADS), 0, stream, a);
+}
+
 cudaError_t launch_paged_append(const PagedAppendArgs& a, bool fp8, int num_sms, cudaStream_t stream)
 {
-    const int per_block = AP_THREADS / (a.d / 8);
-    long long blocks = (static_cast<long long>(a.p.n_tokens) * a.Hk + per_block - 1) / per_block;
-    if (blocks > num_sms * 8ll) blocks = num_sms * 8ll;  // 8 x 256 threads resident per SM
-    if (blocks < 1) blocks = 1;                          // the lengths are still checked
-    auto kern = a.d == 128 ? (fp8 ? paged_append_kernel<16, true> : paged_append_kernel<16, false>)
-                           : (fp8 ? paged_append_kernel<8, true> : paged_append_kernel<8, false>);
-    return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(AP_THREADS), 0, stream, a);
+    // Few rows: one row a lane group, for the shortest chain of one.  From the rows that fill the card (a
+    // block of 256 threads on half of its thread slots) on, several heads a group; in FP8 16 elements a
+    // lane, which halves the work per row (its scale, the shuffles).
+    const bool few = static_cast<long long>(a.p.n_tokens) * a.Hk * (a.d / 8) < num_sms * 1024ll || a.Hk < 2;
+    if (fp8) return few ? launch_append<8, 1, true>(a, stream) : launch_append<16, 2, true>(a, stream);
+    return few ? launch_append<8, 1, false>(a, stream) : launch_append<8, 4, false>(a, stream);
 }
 
 cudaError_t launch_paged_read(const PagedReadArgs& a, cudaStream_t stream)
