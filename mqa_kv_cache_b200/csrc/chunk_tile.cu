@@ -13,9 +13,10 @@
 // Q tile whose even and odd key tiles go to the two softmax groups, each with its own
 // maximum, sum and accumulator, joined from tensor memory at the end.
 //
-// Warps: 0-3 / 4-7 softmax (one thread per query row, its 128 scores in registers),
-// 8 issues the MMAs, 9 loads K/V pages (one box per page and 64-column half, page
-// entries fetched one tile ahead), 10 loads Q, 11 idle.  FP8: warps 12-15 turn the
+// Warps: 0-7 / 8-15 softmax of the two buffers (16 rows a warp, 64 scores a thread: half the
+// time of a thread per row, which the chain scores - softmax - P V - next scores waits for),
+// 16 issues the MMAs, 17 loads K/V pages (one box per page and 64-column half, page entries
+// fetched one tile ahead), 18 loads Q, 19 hands out the pieces.  FP8: warps 20-23 turn the
 // codes of each landed tile into bf16 (exact) in the layout that the MMAs read; the keys'
 // scales multiply the scores and the values' scales the weights, in fp32.
 // TMEM: S0 | S1 | O0 | O1; the weights (bf16) overwrite the first half of their scores
@@ -55,7 +56,7 @@ struct TCfg {
     static constexpr int NS = (FP8 ? 3 : 4) * 2 / HALVES;  // bf16 K/V slots
     static constexpr int LS = FP8 ? 4 / HALVES : 0;        // code slots
     static constexpr int RING = 8;                     // tiles whose page flags (and scales) are kept
-    static constexpr int THREADS = FP8 ? 512 : 384;
+    static constexpr int THREADS = FP8 ? 768 : 640;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_LAND = OFF_KV + NS * TILE;
@@ -69,8 +70,8 @@ struct TCfg {
     // kv_full[NS], kv_empty[NS], land_full[LS], land_empty[LS], q_full, q_empty, s_full[2], p_full[2], pv_done[2],
     // joined[2], piece_full[PIECES], piece_empty[PIECES], done
     static constexpr int NBAR = 2 * NS + 2 * LS + 11 + 2 * PIECES;
-    // warps that take every piece: 8 of the softmax, MMA, K/V loads, Q loads, 4 of the widening
-    static constexpr int TAKERS = FP8 ? 15 : 11;
+    // warps that take every piece: 16 of the softmax, MMA, K/V loads, Q loads, 4 of the widening
+    static constexpr int TAKERS = FP8 ? 23 : 19;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + RING * 4 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
@@ -90,14 +91,31 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(hi) : "r"(y), "r"(0x7b807b80u), "r"(0x80008000u));
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+// Store of 32 columns x 16 lanes: register 2j of thread t goes to lane t / 4, column 4j + t % 4,
+// register 2j + 1 to lane t / 4 + 8 of it.
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
         "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+// 16 lanes x 16 columns (see common.cuh for the shape).
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st_16x256b_x2(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // warp_wait with a first look that asks for the phase alone.
@@ -141,40 +159,6 @@ __device__ __forceinline__ void commit_to(uint32_t elect, uint64_t* bar)
         "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
         "r"(elect)
         : "memory");
-}
-
-// One row's 128 scores -> weights 2^(s sl2 - mu) to TMEM over the scores; returns their sum.
-// Every exponential goes through the hardware unit, where 2^-inf is exactly 0.  It is not
-// what bounds the softmax (without any exponential the kernel takes as long): moving a
-// quarter of them to an FMA polynomial cost 10% by its instructions, and a second body
-// for tiles without a mask another 4% by its size.
-template <bool FP8>
-__device__ __forceinline__ float row_weights(const uint32_t (&sv)[4][32], float sl2, float mu, uint32_t s_addr,
-                                             const float* vs)
-{
-    const float2 sc2 = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
-    float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
-        float4 v4[FP8 ? 8 : 1];
-        if constexpr (FP8) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v4[i] = reinterpret_cast<const float4*>(vs)[c * 8 + i];
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[c][2 * i]), __uint_as_float(sv[c][2 * i + 1])),
-                                        sc2, nmu);
-            float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            acc[i & 3] = __fadd2_rn(acc[i & 3], pr);
-            if constexpr (FP8) pr = __fmul2_rn(pr, (i & 1) ? make_float2(v4[i / 2].z, v4[i / 2].w) : make_float2(v4[i / 2].x, v4[i / 2].y));
-            pk[i] = pack_bf16x2(pr.x, pr.y);
-        }
-        tmem_st16(s_addr + c * 16, pk);
-    }
-    const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
-    return (a01.x + a01.y) + (a23.x + a23.y);
 }
 
 template <int D, bool FP8>
@@ -223,9 +207,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 2);  // the products' commit, and their issuer
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[i], 8);
             mbar_init(&pv_done[i], 1);
-            mbar_init(&joined[i], 8);
+            mbar_init(&joined[i], 16);
         }
         for (int i = 0; i < PIECES; ++i) {
             mbar_init(&piece_full[i], 1);
@@ -235,12 +219,12 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         *s_abort = 0;
         fence_barrier_init();
     }
-    if (warp == 9 && lane == 0) {
+    if (warp == 17 && lane == 0) {
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    if (warp == 8) {
+    if (warp == 16) {
         tmem_alloc(s_tmem, 512);
         tmem_relinquish();
     }
@@ -289,8 +273,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         return pc.rows > 0;
     };
 
-    if (warp == 9) {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+    if (warp == 17) {
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
         // ===== K/V pages: lane i takes box i of a tile (page, and for bf16 its 64-column half) =====
         const int bp_shift = min(p.page_shift, 7);  // rows of a box: a page's, 128 at most
@@ -367,8 +351,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             uint64_t* full = FP8 ? land_full : kv_full;
             for (uint32_t i = x > R ? x - R : 0; i < x; ++i) mbar_wait(&full[i % R], (i / R) & 1);
         }
-    } else if (warp == 10) {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+    } else if (warp == 18) {
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
         // ===== Q: [128 / g tokens][g heads] boxes, one or two tiles a piece =====
         if (lane == 0) {
@@ -389,8 +373,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             }
             if (np > 0) mbar_wait(q_full, (np - 1) & 1);
         }
-    } else if (warp == 8) {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+    } else if (warp == 16) {
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
         // ===== MMA issue =====
         {
@@ -485,13 +469,17 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             mbar_wait(done, 0);
             __syncwarp();
         }
-    } else if (warp < 8) {
-        if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
-        // ===== softmax + epilogue: one thread per row, warps 0-3 buffer 0, warps 4-7 buffer 1 =====
-        const int t = warp >> 2, quarter = warp & 3;
-        const int r = quarter * 32 + lane;  // row of the Q tile = TMEM lane
-        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    } else if (warp < 16) {
+        // registers: 640 threads at 96 = 512 x 104 + 128 x 64; with FP8 768 at 80 = 512 x 96 + 128 x 40 + 128 x 56
+        if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;" ::: "memory");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
+        // ===== softmax + epilogue: warps 0-7 buffer 0, warps 8-15 buffer 1, 16 rows each =====
+        // A row's scores are spread over a lane quad: thread (g, q) = (lane / 4, lane % 4) holds, of rows g and
+        // g + 8 of the warp's 16, the keys 8 j + 2 q and 8 j + 2 q + 1.
+        const int t = warp >> 3, quarter = warp & 3, half = (warp >> 2) & 1;
+        const int r16 = quarter * 32 + half * 16;  // the warp's first row of the Q tile = TMEM lane
+        const int q2 = 2 * (lane & 3);
+        const uint32_t lane_off = static_cast<uint32_t>(r16) << 16;
         const uint32_t s_addr = tmem + lane_off + t * CH_KEYS;
         const uint32_t o_base = tmem + lane_off + 256;
         const float sl2 = a.scale * kLog2e;
@@ -502,12 +490,13 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         for (int n = 0; take(n, u); ++n) {
             const int tb = u.tb, te = u.te;
             const bool pair = u.cost == 2;  // two Q tiles; else one, its key tiles dealt out in turn
-            const int row = pair ? t * 128 + r : r;
-            const int pos = u.pos0 + (row >> gs);
-            const int pos_first = u.pos0 + ((row - lane) >> gs);  // the warp's lowest
-            const bool active_warp = row - lane < u.rows;
+            const int row0 = (pair ? t * 128 : 0) + r16;  // the warp's first row of the block
+            const int rowa = row0 + (lane >> 2), rowb = rowa + 8;
+            const int posa = u.pos0 + (rowa >> gs), posb = u.pos0 + (rowb >> gs);
+            const int pos_first = u.pos0 + (row0 >> gs);
+            const bool active_warp = row0 < u.rows;
             const int n_my = pair ? max((t == 0 ? min(te, u.tiles0) : te) - tb, 0) : (te - tb + 1 - t) / 2;
-            float m_run = -INFINITY, l_run = 0.f;
+            float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;  // maxima of the rows; this thread's share of their sums
             for (int k = 0; k < n_my; ++k, ++cnt) {
                 const int j = pair ? tb + k : tb + 2 * k + t;
                 const uint32_t it = it0 + (j - tb);
@@ -516,77 +505,120 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 const int nv = min(u.keys - j * CH_KEYS, CH_KEYS);
                 if (!FP8 && nv < CH_KEYS) {
                     // rows of V behind the last key in use were not loaded, or hold what nobody may see:
-                    // zeros, so that 0 * garbage cannot reach a sum (the P V waits for this warp)
+                    // zeros, so that 0 * garbage cannot reach a sum (the P V waits for these warps)
                     const uint32_t xv = 2 * it + 1;
                     if (!ready(&kv_full[xv % NS], (xv / NS) & 1, s_abort)) continue;
-                    if (r >= nv) {
-                        uint8_t* v = smem + C::OFF_KV + (xv % NS) * C::TILE + r * 128;
+                    const int vr = (threadIdx.x & 255) >> 1;
+                    if (vr >= nv) {
+                        uint8_t* v = smem + C::OFF_KV + (xv % NS) * C::TILE + vr * 128 + (lane & 1) * 64;
 #pragma unroll
-                        for (int i = 0; i < C::HALVES * 8; ++i)
-                            *reinterpret_cast<uint4*>(v + (i >> 3) * C::BOX + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        for (int i = 0; i < C::HALVES * 4; ++i)
+                            *reinterpret_cast<uint4*>(v + (i >> 2) * C::BOX + (i & 3) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 if (active_warp) {
                     const uint32_t bad = s_bad[it % C::RING];
-                    const float* ks = s_sc + (it % C::RING) * 2 * CH_KEYS;
-                    const int lim = pos - j * CH_KEYS;  // keys 0 .. lim of the tile are seen
+                    const float* ks = s_sc + (it % C::RING) * 2 * CH_KEYS + q2;
                     const bool masked = pos_first - j * CH_KEYS < CH_KEYS - 1 || bad != 0;  // warp-uniform
-                    uint32_t sv[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, sv[c]);
+                    uint32_t sv[2][32];
+                    tmem_ld_16x256b_x8(s_addr, sv[0]);
+                    tmem_ld_16x256b_x8(s_addr + 64, sv[1]);
                     tmem_wait_ld();
-                    float mxc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    tmem_regs_ready(sv[0]);
+                    tmem_regs_ready(sv[1]);
+                    if constexpr (FP8) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_regs_ready(sv[c]);
-                        if constexpr (FP8) {
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 f = *reinterpret_cast<const float2*>(ks + 8 * i);
+                            uint32_t* x = sv[i >> 3] + 4 * (i & 7);
+                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), f);
+                            const float2 z = __fmul2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), f);
+                            x[0] = __float_as_uint(y.x);
+                            x[1] = __float_as_uint(y.y);
+                            x[2] = __float_as_uint(z.x);
+                            x[3] = __float_as_uint(z.y);
+                        }
+                    }
+                    if (masked) {
+                        const int lima = posa - j * CH_KEYS, limb = posb - j * CH_KEYS;  // keys 0 .. lim of the tile are seen
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 k4 = *reinterpret_cast<const float4*>(ks + c * 32 + i);
-                                const float2 y0 = __fmul2_rn(make_float2(__uint_as_float(sv[c][i]), __uint_as_float(sv[c][i + 1])),
-                                                             make_float2(k4.x, k4.y));
-                                const float2 y1 = __fmul2_rn(make_float2(__uint_as_float(sv[c][i + 2]), __uint_as_float(sv[c][i + 3])),
-                                                             make_float2(k4.z, k4.w));
-                                sv[c][i] = __float_as_uint(y0.x);
-                                sv[c][i + 1] = __float_as_uint(y0.y);
-                                sv[c][i + 2] = __float_as_uint(y1.x);
-                                sv[c][i + 3] = __float_as_uint(y1.y);
+                        for (int i = 0; i < 16; ++i) {
+                            uint32_t* x = sv[i >> 3] + 4 * (i & 7);
+                            const bool b = bad >> (i >> 1) & 1u;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                if (b || 8 * i + q2 + e > lima) x[e] = 0xff800000u;  // -inf
+                                if (b || 8 * i + q2 + e > limb) x[2 + e] = 0xff800000u;
                             }
                         }
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c * 32 + i > lim || (bad >> (c * 2 + i / 16) & 1u)) sv[c][i] = 0xff800000u;  // -inf
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2)
-                            mxc[c] = fmax3(mxc[c], __uint_as_float(sv[c][i]), __uint_as_float(sv[c][i + 1]));
                     }
-                    const float mx = fmaxf(fmaxf(mxc[0], mxc[1]), fmaxf(mxc[2], mxc[3])) * sl2;
+                    float xa[2] = {-INFINITY, -INFINITY}, xb[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t* x = sv[i >> 3] + 4 * (i & 7);
+                        xa[i & 1] = fmax3(xa[i & 1], __uint_as_float(x[0]), __uint_as_float(x[1]));
+                        xb[i & 1] = fmax3(xb[i & 1], __uint_as_float(x[2]), __uint_as_float(x[3]));
+                    }
+                    float mxa = fmaxf(xa[0], xa[1]), mxb = fmaxf(xb[0], xb[1]);
+                    mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
+                    mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
+                    mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2)) * sl2;
+                    mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2)) * sl2;
                     // the reference maximum moves (and O with it, for the warp together) only when the
                     // row's maximum has grown by more than 2^8: the weights stay below 2^8
-                    const bool move = mx > m_run + kRescaleThreshold || m_run == -INFINITY;
-                    const float m_new = move ? fmaxf(mx, m_run) : m_run;
-                    const bool rescale = move && m_run != -INFINITY;
-                    if (__any_sync(0xffffffffu, rescale)) {
-                        const float alpha = rescale ? fast_exp2(m_run - m_new) : 1.f;
-                        l_run *= alpha;
+                    const bool mva = mxa > ma + kRescaleThreshold || ma == -INFINITY;
+                    const bool mvb = mxb > mb + kRescaleThreshold || mb == -INFINITY;
+                    const float na = mva ? fmaxf(mxa, ma) : ma, nb = mvb ? fmaxf(mxb, mb) : mb;
+                    const bool rsa = mva && ma != -INFINITY, rsb = mvb && mb != -INFINITY;
+                    if (__any_sync(0xffffffffu, rsa || rsb)) {
+                        const float ala = rsa ? fast_exp2(ma - na) : 1.f, alb = rsb ? fast_exp2(mb - nb) : 1.f;
+                        la *= ala;
+                        lb *= alb;
                         // (the scores of this tile were issued after the last P V had finished)
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t ov[32];
-                            tmem_ld32(o_base + t * D + c * 32, ov);
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t ov[8];
+                            tmem_ld_16x256b_x2(o_base + t * D + c * 16, ov);
                             tmem_wait_ld();
                             tmem_regs_ready(ov);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-                            tmem_st32(o_base + t * D + c * 32, ov);
+                            for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * ((i & 2) ? alb : ala));
+                            tmem_st_16x256b_x2(o_base + t * D + c * 16, ov);
                         }
                     }
-                    m_run = m_new;
-                    const float mu = m_run == -INFINITY ? 0.f : m_run;
-                    l_run += row_weights<FP8>(sv, sl2, mu, s_addr, ks + CH_KEYS);
+                    ma = na;
+                    mb = nb;
+                    // weights 2^(s sl2 - m), to TMEM as bf16 over the scores' first half.  Every exponential goes
+                    // through the hardware unit, where 2^-inf is exactly 0 (it is not what bounds the softmax: moving
+                    // a quarter of them to an FMA polynomial cost 10% by its instructions)
+                    const float2 sc2 = make_float2(sl2, sl2);
+                    const float mua = ma == -INFINITY ? 0.f : -ma, mub = mb == -INFINITY ? 0.f : -mb;
+                    float2 acca = make_float2(0.f, 0.f), accb = acca;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t* x = sv[h] + 4 * i;
+                            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, make_float2(mua, mua));
+                            const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), sc2, make_float2(mub, mub));
+                            float2 pa = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                            float2 pb = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+                            acca = __fadd2_rn(acca, pa);
+                            accb = __fadd2_rn(accb, pb);
+                            if constexpr (FP8) {
+                                const float2 f = *reinterpret_cast<const float2*>(ks + CH_KEYS + h * 64 + 8 * i);
+                                pa = __fmul2_rn(pa, f);
+                                pb = __fmul2_rn(pb, f);
+                            }
+                            pk[2 * i] = pack_bf16x2(pa.x, pa.y);
+                            pk[2 * i + 1] = pack_bf16x2(pb.x, pb.y);
+                        }
+                        tmem_st_16x128b_x8(s_addr + h * 32, pk);
+                    }
+                    la += acca.x + acca.y;
+                    lb += accb.x + accb.y;
                     tmem_wait_st();
                 }
                 tc_fence_before();
@@ -594,75 +626,95 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 if (lane == 0) mbar_arrive(&p_full[t]);
             }
             it0 += te - tb;
+            la += __shfl_xor_sync(0xffffffffu, la, 1);
+            lb += __shfl_xor_sync(0xffffffffu, lb, 1);
+            la += __shfl_xor_sync(0xffffffffu, la, 2);
+            lb += __shfl_xor_sync(0xffffffffu, lb, 2);
             const bool ok = n_my == 0 || ready(&pv_done[t], (cnt - 1) & 1, s_abort);
             tc_fence_after();
             // ---- the piece's rows: finished, or a partial for the merge ----
-            const long long orow = (static_cast<long long>(u.tok0) + (row >> gs)) * a.H +
-                                   static_cast<long long>(u.kvh) * a.g + (row & (a.g - 1));
-            const long long prow = static_cast<long long>(2 * c + u.first) * CH_ROWS + row;
-            const bool use = ok && row < u.rows;
-            float m = m_run, l = l_run, w0 = 1.f, w1 = 0.f;  // weights of this buffer's (w0) and the other's sums
-            int c0 = 0, c1 = D / 32;
+            float va = 0.f, vb = 0.f;  // weights of the other buffer's sums; ua, ub of this one's (nothing seen: 0, as
+            float ua = ma == -INFINITY ? 0.f : 1.f, ub = mb == -INFINITY ? 0.f : 1.f;  // it may never have been written)
+            int c0 = 0, c1 = D / 16;   // column pieces of 16
             if (!pair) {
                 // join the two buffers: each group writes half of the columns
-                s_ml[t * 128 + r] = make_float2(m_run, l_run);
+                if ((lane & 3) == 0) {
+                    s_ml[t * 128 + r16 + (lane >> 2)] = make_float2(ma, la);
+                    s_ml[t * 128 + r16 + (lane >> 2) + 8] = make_float2(mb, lb);
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&joined[0]);
                 ready(&joined[0], joins & 1, s_abort);
                 tc_fence_after();
-                const float2 o = s_ml[(t ^ 1) * 128 + r];
-                m = fmaxf(m_run, o.x);
-                const float mu = m == -INFINITY ? 0.f : m;
-                w0 = m_run == -INFINITY ? 0.f : fast_exp2(m_run - mu);
-                w1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - mu);
-                l = w0 * l_run + w1 * o.y;
-                c0 = t * (D / 64);
-                c1 = c0 + D / 64;
-            } else if (m_run == -INFINITY) {
-                w0 = 0.f;  // nothing seen: the accumulator may never have been written
+                const float2 oa = s_ml[(t ^ 1) * 128 + r16 + (lane >> 2)], ob = s_ml[(t ^ 1) * 128 + r16 + (lane >> 2) + 8];
+                const float Ma = fmaxf(ma, oa.x), Mb = fmaxf(mb, ob.x);
+                const float fa = Ma == -INFINITY ? 0.f : Ma, fb = Mb == -INFINITY ? 0.f : Mb;
+                ua = fast_exp2(ma - fa);
+                ub = fast_exp2(mb - fb);
+                va = fast_exp2(oa.x - fa);
+                vb = fast_exp2(ob.x - fb);
+                la = ua * la + va * oa.y;
+                lb = ub * lb + vb * ob.y;
+                ma = Ma;
+                mb = Mb;
+                c0 = t * (D / 32);
+                c1 = c0 + D / 32;
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            if (u.count == 1) {
-                w0 *= inv;
-                w1 *= inv;
+            const bool whole = u.count == 1;
+            if (whole) {
+                const float ia = la > 0.f ? 1.f / la : 0.f, ib = lb > 0.f ? 1.f / lb : 0.f;
+                ua *= ia;
+                va *= ia;
+                ub *= ib;
+                vb *= ib;
             }
+            const long long base = static_cast<long long>(u.tok0) * a.H + static_cast<long long>(u.kvh) * a.g;
+            const long long outa = base + static_cast<long long>(rowa >> gs) * a.H + (rowa & (a.g - 1));
+            const long long outb = base + static_cast<long long>(rowb >> gs) * a.H + (rowb & (a.g - 1));
+            const long long part = static_cast<long long>(2 * c + u.first) * CH_ROWS;
+            const bool usea = ok && rowa < u.rows, useb = ok && rowb < u.rows;
 #pragma unroll 1
             for (int cc = c0; cc < c1; ++cc) {
-                uint32_t ov[32];
-                tmem_ld32(o_base + t * D + cc * 32, ov);
+                uint32_t ov[8];
+                tmem_ld_16x256b_x2(o_base + t * D + cc * 16, ov);
                 tmem_wait_ld();
                 tmem_regs_ready(ov);
+                float x[8];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) ov[i] = w0 == 0.f ? 0u : __float_as_uint(__uint_as_float(ov[i]) * w0);
-                if (!pair) {
-                    uint32_t ow[32];
-                    tmem_ld32(o_base + (t ^ 1) * D + cc * 32, ow);
-                    tmem_wait_ld();
-                    tmem_regs_ready(ow);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (w1 != 0.f) ov[i] = __float_as_uint(fmaf(__uint_as_float(ow[i]), w1, __uint_as_float(ov[i])));
+                for (int i = 0; i < 8; ++i) {
+                    const float f = (i & 2) ? ub : ua;
+                    x[i] = f == 0.f ? 0.f : __uint_as_float(ov[i]) * f;
                 }
-                if (use && u.count == 1) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + cc * 32);
+                if (!pair) {
+                    tmem_ld_16x256b_x2(o_base + (t ^ 1) * D + cc * 16, ov);
+                    tmem_wait_ld();
+                    tmem_regs_ready(ov);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        dst[i / 8] = make_uint4(pack_bf16x2(__uint_as_float(ov[i]), __uint_as_float(ov[i + 1])),
-                                                pack_bf16x2(__uint_as_float(ov[i + 2]), __uint_as_float(ov[i + 3])),
-                                                pack_bf16x2(__uint_as_float(ov[i + 4]), __uint_as_float(ov[i + 5])),
-                                                pack_bf16x2(__uint_as_float(ov[i + 6]), __uint_as_float(ov[i + 7])));
-                } else if (use) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + cc * 32);
+                    for (int i = 0; i < 8; ++i) {
+                        const float f = (i & 2) ? vb : va;
+                        if (f != 0.f) x[i] = fmaf(__uint_as_float(ov[i]), f, x[i]);
+                    }
+                }
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) dst[i / 4] = make_uint4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+                for (int i = 0; i < 2; ++i) {
+                    const int col = cc * 16 + 8 * i + q2;
+                    if (whole) {
+                        if (usea) *reinterpret_cast<uint32_t*>(a.out + outa * D + col) = pack_bf16x2(x[4 * i], x[4 * i + 1]);
+                        if (useb) *reinterpret_cast<uint32_t*>(a.out + outb * D + col) = pack_bf16x2(x[4 * i + 2], x[4 * i + 3]);
+                    } else {
+                        if (usea) *reinterpret_cast<float2*>(a.part_o + (part + rowa) * D + col) = make_float2(x[4 * i], x[4 * i + 1]);
+                        if (useb) *reinterpret_cast<float2*>(a.part_o + (part + rowb) * D + col) = make_float2(x[4 * i + 2], x[4 * i + 3]);
+                    }
                 }
             }
-            if (use && (pair || t == 0)) {
-                if (u.count == 1) {
-                    if (a.lse) a.lse[orow] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+            if ((lane & 3) == 0 && (pair || t == 0)) {
+                if (whole) {
+                    if (a.lse && usea) a.lse[outa] = la > 0.f ? (ma + __log2f(la)) * kLn2 : -INFINITY;
+                    if (a.lse && useb) a.lse[outb] = lb > 0.f ? (mb + __log2f(lb)) * kLn2 : -INFINITY;
                 } else {
-                    a.part_ml[prow] = make_float2(m, l);
+                    if (usea) a.part_ml[part + rowa] = make_float2(ma, la);
+                    if (useb) a.part_ml[part + rowb] = make_float2(mb, lb);
                 }
             }
             // the other group reads this buffer's accumulator: the next piece waits for it
@@ -674,12 +726,12 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 ++joins;
             }
         }
-    } else if (warp >= 12) {
+    } else if (warp >= 20) {
         if constexpr (FP8) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
             // ===== codes -> bf16 tiles in the 128-byte-swizzled layout =====
             constexpr int CH = D / 16;  // 16-code chunks per row
-            const int tid = threadIdx.x - 384;
+            const int tid = threadIdx.x - 640;
             uint32_t x = 0;
             bool ok = true;
             Piece u;
@@ -728,9 +780,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             }
         }
     } else {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
-        // ===== warp 11: this CTA's pieces =====
+        // ===== warp 19: this CTA's pieces =====
         if (lane == 0) {
             const long long N = plan.total();
             // every CTA's stretch holds two points at least, so that it owns a tile of each unit it lies in
@@ -776,7 +828,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
