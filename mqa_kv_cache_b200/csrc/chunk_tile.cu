@@ -65,19 +65,46 @@ struct TCfg {
     static constexpr int OFF_CU = OFF_U + (PAGED_MAX_B + 1) * 8;
     static constexpr int OFF_LEN = OFF_CU + (PAGED_MAX_B + 1) * 4;
     static constexpr int OFF_ML = (OFF_LEN + PAGED_MAX_B * 4 + 15) / 16 * 16;  // [2][128] (max, sum)
-    static constexpr int OFF_PIECE = OFF_ML + 2 * 128 * 8;
+    static constexpr int OFF_QS = OFF_ML + 2 * 128 * 8;  // [2 pieces][256] powers of two that Q's rows were divided by (FP8)
+    static constexpr int OFF_PIECE = OFF_QS + (FP8 ? 2 * CH_ROWS * 4 : 0);
     static constexpr int OFF_BAR = OFF_PIECE + PIECES * static_cast<int>(sizeof(Piece));
     // kv_full[NS], kv_empty[NS], land_full[LS], land_empty[LS], q_full, q_empty, s_full[2], p_full[2], pv_done[2],
-    // joined[2], piece_full[PIECES], piece_empty[PIECES], done
-    static constexpr int NBAR = 2 * NS + 2 * LS + 11 + 2 * PIECES;
+    // joined[2], piece_full[PIECES], piece_empty[PIECES], done, q_ready
+    static constexpr int NBAR = 2 * NS + 2 * LS + 12 + 2 * PIECES;
     // warps that take every piece: 16 of the softmax, MMA, K/V loads, Q loads, 4 of the widening
     static constexpr int TAKERS = FP8 ? 23 : 19;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + RING * 4 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
-    static constexpr uint32_t IDESC_S = umma_idesc_bf16(128, CH_KEYS);
+    // Q x K in bf16, or in fp16 with FP8 (formats 0 instead of 1 in bits 7 and 10)
+    static constexpr uint32_t IDESC_S = umma_idesc_bf16(128, CH_KEYS) & (FP8 ? ~((1u << 7) | (1u << 10)) : ~0u);
     static constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D, false, true);
 };
+
+// 2^x for two values on the FMA pipe (Cody-Waite split x = n + f, n = rint(x)); 0 below -125.
+// Degree-4 polynomial for 2^f on [-1/2, 1/2], minimax in relative error (2.7e-6 in fp32 Horner
+// form), produced by fit_exp2_poly.py's remez(4): the sums enter an fp32 output (lse), which the
+// degree-3 one's 7.5e-5 would show in.
+__device__ __forceinline__ float2 exp2_poly2(float2 x)
+{
+    const float2 t = __fadd2_rn(x, make_float2(kShifter, kShifter));
+    const float2 n = __fadd2_rn(t, make_float2(-kShifter, -kShifter));
+    const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
+    float2 p = __ffma2_rn(make_float2(0.009570102f, 0.009570102f), f, make_float2(0.05591786f, 0.05591786f));
+    p = __ffma2_rn(p, f, make_float2(0.24024744f, 0.24024744f));
+    p = __ffma2_rn(p, f, make_float2(0.6931218f, 0.6931218f));
+    p = __ffma2_rn(p, f, make_float2(0.9999993f, 0.9999993f));
+    return make_float2(x.x < -125.f ? 0.f : __uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                       x.y < -125.f ? 0.f : __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// Four E4M3 codes -> fp16 pairs, exactly.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
 
 // Four E4M3 codes -> bf16 pairs, exactly: the code's sign, exponent and mantissa bits at
 // bf16's places stand for 2^-120 of its value (subnormal codes are bf16 subnormals then),
@@ -183,6 +210,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
     uint64_t* piece_full = q_full + 10;
     uint64_t* piece_empty = piece_full + PIECES;
     uint64_t* done = piece_empty + PIECES;
+    uint64_t* q_ready = done + 1;  // FP8: Q's rows are fp16
+    float* s_qs = reinterpret_cast<float*>(smem + C::OFF_QS);
     const Piece* s_piece = reinterpret_cast<const Piece*>(smem + C::OFF_PIECE);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -216,6 +245,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             mbar_init(&piece_empty[i], C::TAKERS);
         }
         mbar_init(done, 1);
+        mbar_init(q_ready, 4);
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -419,7 +449,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             Piece u;
             while (ok && take(np, u)) {
                 const int tb = u.tb, te = u.te;
-                ok = ready(q_full, np & 1, s_abort);
+                ok = ready(FP8 ? q_ready : q_full, np & 1, s_abort);
                 ++np;
                 if (!ok) break;
                 const int n = te - tb;
@@ -496,6 +526,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             const int pos_first = u.pos0 + (row0 >> gs);
             const bool active_warp = row0 < u.rows;
             const int n_my = pair ? max((t == 0 ? min(te, u.tiles0) : te) - tb, 0) : (te - tb + 1 - t) / 2;
+            float sl2a = sl2, sl2b = sl2;  // raw scores to log2 units
             float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;  // maxima of the rows; this thread's share of their sums
             for (int k = 0; k < n_my; ++k, ++cnt) {
                 const int j = pair ? tb + k : tb + 2 * k + t;
@@ -516,6 +547,11 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                             *reinterpret_cast<uint4*>(v + (i >> 2) * C::BOX + (i & 3) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                if (FP8 && k == 0) {  // (the scores wait for the converted Q rows)
+                    const float* qs = s_qs + (n & 1) * CH_ROWS + row0 + (lane >> 2);
+                    sl2a = sl2 * qs[0];
+                    sl2b = sl2 * qs[8];
                 }
                 if (active_warp) {
                     const uint32_t bad = s_bad[it % C::RING];
@@ -563,8 +599,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     float mxa = fmaxf(xa[0], xa[1]), mxb = fmaxf(xb[0], xb[1]);
                     mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
                     mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
-                    mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2)) * sl2;
-                    mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2)) * sl2;
+                    mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2)) * sl2a;
+                    mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2)) * sl2b;
                     // the reference maximum moves (and O with it, for the warp together) only when the
                     // row's maximum has grown by more than 2^8: the weights stay below 2^8
                     const bool mva = mxa > ma + kRescaleThreshold || ma == -INFINITY;
@@ -589,10 +625,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     }
                     ma = na;
                     mb = nb;
-                    // weights 2^(s sl2 - m), to TMEM as bf16 over the scores' first half.  Every exponential goes
-                    // through the hardware unit, where 2^-inf is exactly 0 (it is not what bounds the softmax: moving
-                    // a quarter of them to an FMA polynomial cost 10% by its instructions)
-                    const float2 sc2 = make_float2(sl2, sl2);
+                    // weights 2^(s sl2 - m), to TMEM as bf16 over the scores' first half.  bf16: a quarter of the
+                    // exponentials on the FMA pipe (none / an eighth / a quarter / half of them there: 704 / 706 / 686 /
+                    // 735 us for two 3.5K-token chunks; FP8 is bound by instructions: none)
+                    const float2 sca = make_float2(sl2a, sl2a), scb = make_float2(sl2b, sl2b);
                     const float mua = ma == -INFINITY ? 0.f : -ma, mub = mb == -INFINITY ? 0.f : -mb;
                     float2 acca = make_float2(0.f, 0.f), accb = acca;
 #pragma unroll
@@ -601,10 +637,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const uint32_t* x = sv[h] + 4 * i;
-                            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, make_float2(mua, mua));
-                            const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), sc2, make_float2(mub, mub));
+                            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sca, make_float2(mua, mua));
+                            const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), scb, make_float2(mub, mub));
                             float2 pa = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                            float2 pb = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+                            float2 pb = !FP8 && (i & 1) == 0 ? exp2_poly2(z) : make_float2(fast_exp2(z.x), fast_exp2(z.y));
                             acca = __fadd2_rn(acca, pa);
                             accb = __fadd2_rn(accb, pb);
                             if constexpr (FP8) {
@@ -729,16 +765,51 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
     } else if (warp >= 20) {
         if constexpr (FP8) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
-            // ===== codes -> bf16 tiles in the 128-byte-swizzled layout =====
-            constexpr int CH = D / 16;  // 16-code chunks per row
-            const int tid = threadIdx.x - 640;
+            // ===== Q -> fp16 in place; codes -> 16-bit tiles in the 128-byte-swizzled layout: K fp16, V bf16 =====
+            // K's products need no range beyond Q's and the codes', and fp16 is one conversion for two codes; the
+            // weights, times the values' scales, need bf16's.
+            const int tid = threadIdx.x - 640, cwarp = tid >> 5;
+            // chunk of 16 codes: two rows by four chunks in eight neighbouring lanes, so that either half of their
+            // 32 bytes falls on eight different bank groups
+            const int ch0 = lane & 3, row0 = ((lane >> 2) & 1) + ((lane >> (D == 128 ? 4 : 3)) << 1);
+            const int ch = ch0 + (D == 128 ? (lane >> 1) & 4 : 0);
+            constexpr int RW = D == 128 ? 4 : 8;  // rows a warp takes at a time
             uint32_t x = 0;
             bool ok = true;
             Piece u;
             for (int n = 0; ok && take(n, u); ++n) {
+                // a row's 16-byte pieces lie in D / 8 neighbouring lanes
+                ok = ready(q_full, n & 1, s_abort);
+                if (!ok) break;
+#pragma unroll 2
+                for (int i = 0; i < u.cost * 128 * (D / 8) / 128; ++i) {
+                    const int id = i * 128 + tid, row = id / (D / 8), c8 = id % (D / 8);
+                    uint4* q = reinterpret_cast<uint4*>(smem + C::OFF_Q + (row >> 7) * C::TILE + (c8 >> 3) * C::BOX + swz128(row & 127, c8 & 7));
+                    const uint4 v = *q;
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    float m = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m = fmax3(m, fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e])));
+#pragma unroll
+                    for (int o = D / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    // largest element to [2^14, 2^15): an element below 2^-29 of it rounds to a multiple of 2^-40 of
+                    // it, far below the fp32 sums' own rounding; two factors, as one may leave fp32's range
+                    const int ex = m > 0.f ? 14 - ilogbf(m) : 0;
+                    const float fa = ldexpf(1.f, ex / 2), fb = ldexpf(1.f, ex - ex / 2);
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[e]) : "f"(bf16_hi(w[e]) * fa * fb), "f"(bf16_lo(w[e]) * fa * fb));
+                    *q = make_uint4(o[0], o[1], o[2], o[3]);
+                    if (c8 == 0) s_qs[(n & 1) * CH_ROWS + row] = ldexpf(1.f, -ex);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_ready);
                 for (int j = u.tb; j < u.te && ok; ++j) {
                     const int nv = min(u.keys - j * CH_KEYS, CH_KEYS);
                     const uint32_t it = x / 2;
+#pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++x) {
                         const uint32_t ls = x % (LS > 0 ? LS : 1), slot = x % NS;
                         ok = ready(&land_full[ls], (x / (LS > 0 ? LS : 1)) & 1, s_abort);
@@ -752,22 +823,26 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                             sc[CH_KEYS] = 0.f;
                         }
                         const uint8_t* src = smem + C::OFF_LAND + ls * C::CODES;
-                        uint8_t* dst = smem + C::OFF_KV + slot * C::TILE;
+                        uint8_t* dst = smem + C::OFF_KV + slot * C::TILE + (ch >> 2) * C::BOX;
 #pragma unroll 2
-                        for (int i = 0; i < CH; ++i) {
-                            const int id = i * 128 + tid, row = id / CH, ch = id % CH;
-                            const uint4 v = *reinterpret_cast<const uint4*>(src + id * 16);
+                        for (int i = 0; i < CH_KEYS / (4 * RW); ++i) {
+                            const int row = (i * 4 + cwarp) * RW + row0;
+                            const uint4 v = *reinterpret_cast<const uint4*>(src + row * D + ch * 16);
                             uint4 o0, o1;
-                            codes_to_bf16(v.x, o0.x, o0.y);
-                            codes_to_bf16(v.y, o0.z, o0.w);
-                            codes_to_bf16(v.z, o1.x, o1.y);
-                            codes_to_bf16(v.w, o1.z, o1.w);
-                            if (kv == 1 && partial && row >= nv) o0 = o1 = make_uint4(0, 0, 0, 0);
-                            uint8_t* d = dst + (ch >> 2) * C::BOX;
-                            // chunks of the upper half in the other order: their banks are the lower half's
-                            const int sw = ch >> 2, c0 = (ch & 3) * 2;
-                            *reinterpret_cast<uint4*>(d + swz128(row, c0 + sw)) = sw ? o1 : o0;
-                            *reinterpret_cast<uint4*>(d + swz128(row, c0 + (sw ^ 1))) = sw ? o0 : o1;
+                            if (kv == 0) {
+                                codes_to_f16(v.x, o0.x, o0.y);
+                                codes_to_f16(v.y, o0.z, o0.w);
+                                codes_to_f16(v.z, o1.x, o1.y);
+                                codes_to_f16(v.w, o1.z, o1.w);
+                            } else {
+                                codes_to_bf16(v.x, o0.x, o0.y);
+                                codes_to_bf16(v.y, o0.z, o0.w);
+                                codes_to_bf16(v.z, o1.x, o1.y);
+                                codes_to_bf16(v.w, o1.z, o1.w);
+                                if (partial && row >= nv) o0 = o1 = make_uint4(0, 0, 0, 0);
+                            }
+                            *reinterpret_cast<uint4*>(dst + swz128(row, 2 * ch0)) = o0;
+                            *reinterpret_cast<uint4*>(dst + swz128(row, 2 * ch0 + 1)) = o1;
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
