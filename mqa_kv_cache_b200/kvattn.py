@@ -685,32 +685,36 @@ _lib.attn_chunk_paged_fp8.argtypes = _chunk_head + [_vp, _vp, _vp, _vp, _f32, _v
 
 
 # A decode step's kernels here run for a few microseconds, so these wrappers keep to one pass of cheap
-# checks and hand plain integers to the library; what fails a check goes to _paged_refuse for its error.
+# checks and hand plain integers to the library; whatever fails them goes to _paged_refuse for its error.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_bf16, _f32, _i32t, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _paged_refuse(dev, t, dtype, name):
-    _need(t, dtype, name)
-    _contig(t, name)
-    raise ValueError(f"{name} is on another device")
+def _paged_refuse(dev, *tensors):
+    """The error of the first (tensor, dtype, name) that is not a contiguous CUDA tensor of its type on `dev`."""
+    for t, dtype, name in tensors:
+        _need(t, dtype, name)
+        _contig(t, name)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on another device")
 
 
 def _paged_ptr(dev, t, dtype, name):
     """The address of a contiguous CUDA tensor of that type on device `dev`."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        _paged_refuse(dev, t, dtype, name)
+        _paged_refuse(dev, (t, dtype, name))
     return t.data_ptr()
 
 
 def _paged_tokens(x, name):
     """(shape, token stride, device) of packed head vectors [n_tokens, heads, d]: heads contiguous, any
     token stride (slices of a fused projection).  The device has to be the current one."""
-    if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or x.get_device() < 0:
-        _need(x, torch.bfloat16, name)
-    if x.dim() != 3:
-        raise ValueError(f"{name} must be [n_tokens, heads, head_dim]")
+    if not isinstance(x, torch.Tensor) or x.dtype is not _bf16 or not x.is_cuda:
+        _need(x, _bf16, name)
     shape = x.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [n_tokens, heads, head_dim]")
     T, H, d = shape
     st, sh, sd = x.stride()
     if (sd != 1 and d > 1) or (sh != d and H > 1):
@@ -723,41 +727,57 @@ def _paged_tokens(x, name):
 
 def _paged_batch(dev, cu, seq_lens, page_table):
     """(addresses of a batch's tensors, B, max_pages)."""
-    i32 = torch.int32
-    ptrs = (None if cu is None else _paged_ptr(dev, cu, i32, "cu"), _paged_ptr(dev, seq_lens, i32, "seq_lens"),
-            _paged_ptr(dev, page_table, i32, "page_table"))
-    if page_table.dim() != 2:
+    if cu is None:
+        cu_p = None
+    else:
+        cu_p = _paged_ptr(dev, cu, _i32t, "cu")
+    try:
+        good = (seq_lens.dtype is _i32t and page_table.dtype is _i32t and seq_lens.is_contiguous()
+                and page_table.is_contiguous() and seq_lens.get_device() == dev and page_table.get_device() == dev)
+    except AttributeError:
+        good = False
+    if not good:
+        _paged_refuse(dev, (seq_lens, _i32t, "seq_lens"), (page_table, _i32t, "page_table"))
+    shape = page_table.shape
+    if len(shape) != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    B, max_pages = page_table.shape
+    B, max_pages = shape
     if seq_lens.numel() != B or (cu is not None and cu.numel() != B + 1):
         raise ValueError("seq_lens must hold B entries and cu B + 1")
-    return ptrs, B, max_pages
+    return (cu_p, seq_lens.data_ptr(), page_table.data_ptr()), B, max_pages
 
 
-def _paged_caches(dev, fp8, k, v, ks, vs, Hk, d):
-    """(addresses in the library's order, n_pages, page size) of a cache [n_pages, Hk, page, d] and its scales;
-    Hk None: any."""
+def _paged_caches(dev, fp8, k, v, ks, vs, d):
+    """(addresses in the library's order, n_pages, Hk, page size) of a cache [n_pages, Hk, page, d] and its scales."""
+    rows = _u8 if fp8 else _bf16
+    try:
+        good = (k.dtype is rows and v.dtype is rows and k.is_contiguous() and v.is_contiguous()
+                and k.get_device() == dev and v.get_device() == dev)
+        if fp8:
+            good = (good and ks.dtype is _f32 and vs.dtype is _f32 and ks.is_contiguous() and vs.is_contiguous()
+                    and ks.get_device() == dev and vs.get_device() == dev)
+    except AttributeError:
+        good = False
     kn, vn = ("k_codes", "v_codes") if fp8 else ("k_pages", "v_pages")
-    rows = torch.uint8 if fp8 else torch.bfloat16
-    kp, vp = _paged_ptr(dev, k, rows, kn), _paged_ptr(dev, v, rows, vn)
+    if not good:
+        _paged_refuse(dev, (k, rows, kn), (v, rows, vn), *(((ks, _f32, "k_scales"), (vs, _f32, "v_scales")) if fp8 else ()))
     shape = k.shape
     if len(shape) != 4:
         raise ValueError(f"{kn} must be [n_pages, n_kv_head, page_size, head_dim]")
+    n_pages, Hk, page, dk = shape
     if v.shape != shape:
         raise ValueError(f"inconsistent shape of {vn}")
-    if shape[3] != d or (Hk is not None and shape[1] != Hk):
+    if dk != d:
         raise ValueError(f"inconsistent shape of {kn}")
     if not fp8:
-        return (kp, vp), shape[0], shape[2]
-    f32 = torch.float32
-    ksp, vsp = _paged_ptr(dev, ks, f32, "k_scales"), _paged_ptr(dev, vs, f32, "v_scales")
-    if ks.shape != shape[:3] or vs.shape != shape[:3]:
+        return (k.data_ptr(), v.data_ptr()), n_pages, Hk, page
+    if ks.shape != (n_pages, Hk, page) or vs.shape != (n_pages, Hk, page):
         raise ValueError("inconsistent shape of the scales")
-    return (kp, ksp, vp, vsp), shape[0], shape[2]
+    return (k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr()), n_pages, Hk, page
 
 
 def _status_ptr(dev, t):
-    return None if t is None else _paged_ptr(dev, t, torch.int32, "dev_status")
+    return None if t is None else _paged_ptr(dev, t, _i32t, "dev_status")
 
 
 def _append_paged(fn, fp8, k_new, v_new, cu, seq_lens, page_table, k, ks, v, vs, cos, sin, pair_style, dev_status):
@@ -767,9 +787,10 @@ def _append_paged(fn, fp8, k_new, v_new, cu, seq_lens, page_table, k, ks, v, vs,
     if v_shape != shape:
         raise ValueError("inconsistent append shapes")
     (cu_p, len_p, pt_p), B, max_pages = _paged_batch(dev, cu, seq_lens, page_table)
-    caches, n_pages, page = _paged_caches(dev, fp8, k, v, ks, vs, Hk, d)
-    f32 = torch.float32
-    cos_p, sin_p = _paged_ptr(dev, cos, f32, "cos"), _paged_ptr(dev, sin, f32, "sin")
+    caches, n_pages, heads, page = _paged_caches(dev, fp8, k, v, ks, vs, d)
+    if heads != Hk:
+        raise ValueError("inconsistent append shapes")
+    cos_p, sin_p = _paged_ptr(dev, cos, _f32, "cos"), _paged_ptr(dev, sin, _f32, "sin")
     if cos.dim() != 2 or cos.shape[1] * 2 != d or sin.shape != cos.shape:
         raise ValueError("tables must be [max_pos, d/2]")
     rc = fn(k_new.data_ptr(), k_st, v_new.data_ptr(), v_st, cu_p, len_p, pt_p, B, T, Hk, d, page, max_pages, n_pages,
@@ -808,8 +829,8 @@ def kv_read_paged_fp8(k_codes, k_scales, v_codes, v_scales, page_table, seq_lens
         raise ValueError("k_out and v_out must be [B, n_kv_head, T_max, head_dim]")
     Bo, Hk, T_max, d = k_out.shape
     (_, len_p, pt_p), B, max_pages = _paged_batch(dev, None, seq_lens, page_table)
-    (kp, ksp, vp, vsp), n_pages, page = _paged_caches(dev, True, k_codes, v_codes, k_scales, v_scales, Hk, d)
-    if Bo != B:
+    (kp, ksp, vp, vsp), n_pages, heads, page = _paged_caches(dev, True, k_codes, v_codes, k_scales, v_scales, d)
+    if Bo != B or heads != Hk:
         raise ValueError("inconsistent read shapes")
     rc = _lib.kv_read_paged_fp8(kp, ksp, vp, vsp, pt_p, len_p, B, Hk, d, page, max_pages, n_pages, T_max, ko, vo,
                                 _status_ptr(dev, dev_status), _raw_stream(dev))
@@ -825,21 +846,20 @@ def _chunk_paged(fn, fp8, q, cu, seq_lens, page_table, k, ks, v, vs, scale, max_
     shape, q_st, dev = _paged_tokens(q, "q")
     T, H, d = shape
     (cu_p, len_p, pt_p), B, max_pages = _paged_batch(dev, cu, seq_lens, page_table)
-    caches, n_pages, page = _paged_caches(dev, fp8, k, v, ks, vs, None, d)
-    Hk = k.shape[1]
+    caches, n_pages, Hk, page = _paged_caches(dev, fp8, k, v, ks, vs, d)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_strided(shape, (H * d, d, 1), dtype=_bf16, device=q.device)
         out_p = out.data_ptr()
     else:
-        out_p = _paged_ptr(dev, out, torch.bfloat16, "out")
+        out_p = _paged_ptr(dev, out, _bf16, "out")
         if out.shape != shape:
             raise ValueError("out must have the shape of q")
     if lse is not None:
-        lse_p = _paged_ptr(dev, lse, torch.float32, "lse")
+        lse_p = _paged_ptr(dev, lse, _f32, "lse")
         if lse.shape != (T, H):
             raise ValueError("lse must be [n_tokens, n_head]")
     elif want_lse:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = torch.empty_strided((T, H), (H, 1), dtype=_f32, device=q.device)
         lse_p = lse.data_ptr()
     else:
         lse_p = None
@@ -847,7 +867,7 @@ def _chunk_paged(fn, fp8, q, cu, seq_lens, page_table, k, ks, v, vs, scale, max_
     if ws is None:
         ws = workspace(attn_chunk_paged_workspace_bytes(B, T, max_q, H, Hk, d), q.device)
     rc = fn(q.data_ptr(), q_st, cu_p, len_p, pt_p, B, T, max_q, H, Hk, d, page, max_pages, n_pages, *caches, float(scale),
-            out_p, lse_p, _paged_ptr(dev, ws, torch.uint8, "ws"), ws.numel(), _status_ptr(dev, dev_status),
+            out_p, lse_p, _paged_ptr(dev, ws, _u8, "ws"), ws.numel(), _status_ptr(dev, dev_status),
             _raw_stream(dev))
     if rc:
         _check(rc)
