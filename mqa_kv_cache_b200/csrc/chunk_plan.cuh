@@ -18,23 +18,24 @@ namespace kvattn {
 constexpr int CH_ROWS = 256;  // query rows of a block
 constexpr int CH_KEYS = 128;  // keys of a tile
 
-// sum over i = 1 .. k of the tiles that base + i w keys fill (w a power of two, 4 .. 256).
-__host__ __device__ inline long long chunk_tiles_prefix(int base, int w, int k)
+// Sums in closed form, by shifts: one thread walks the plan at the head of every call.
+// Sum over i = 1 .. k of the tiles that base + i w keys fill, w = 1 << ws (4 .. 256).
+__host__ __device__ inline long long chunk_tiles_prefix(int base, int ws, int k)
 {
     int first = 1;  // the blocks before it end at or before row 0
-    if (base < 0) first = -base / w + 1;
+    if (base < 0) first = (-base >> ws) + 1;
     if (k < first) return 0;
     const long long n = k - first + 1;
-    const int x0 = base + (first - 1) * w;  // > -w, and x0 + w > 0
-    if (w >= CH_KEYS) {
-        const long long c0 = x0 > 0 ? (x0 + CH_KEYS - 1) / CH_KEYS : -(-x0 / CH_KEYS);
-        return n * c0 + (w / CH_KEYS) * (n * (n + 1) / 2);
+    const int x0 = base + ((first - 1) << ws);  // > -w, and x0 + w > 0
+    if (ws >= 7) {
+        const long long c0 = x0 > 0 ? (x0 + CH_KEYS - 1) >> 7 : -(-x0 >> 7);
+        return n * c0 + ((n * (n + 1) / 2) << (ws - 7));
     }
-    const long long m = CH_KEYS / w;                      // blocks per tile of keys
-    const long long r = x0 > 0 ? (x0 + w - 1) / w : 0;    // ceil((x0 + i w) / 128) = ceil((r + i) / m)
-    auto upto = [m](long long x) {                        // sum of ceil(i / m), i = 1 .. x
-        const long long q = x / m;
-        return m * q * (q + 1) / 2 + (x - q * m) * (q + 1);
+    const int ms = 7 - ws;                                              // m = 1 << ms blocks per tile of keys
+    const long long r = x0 > 0 ? (x0 + (1 << ws) - 1) >> ws : 0;        // ceil((x0 + i w) / 128) = ceil((r + i) / m)
+    auto upto = [ms](long long x) {                                     // sum of ceil(i / m), i = 1 .. x
+        const long long q = x >> ms;
+        return ((q * (q + 1) / 2) << ms) + (x - (q << ms)) * (q + 1);
     };
     return upto(r + n) - upto(r);
 }
@@ -42,18 +43,27 @@ __host__ __device__ inline long long chunk_tiles_prefix(int base, int w, int k)
 struct ChunkSeq {
     int t0, n, take, len;  // packed tokens t0 .. t0 + take - 1 are computed (take = min(n, max_q))
     __host__ __device__ int base() const { return len - n; }
-    // cost of this sequence's blocks 0 .. k - 1 on one KV head
-    __host__ __device__ long long cost(int k, int w, int g) const
+    // cost of this sequence's blocks 0 .. k - 1 on one KV head, blocks of 1 << ws tokens (256 rows)
+    __host__ __device__ long long cost(int k, int ws) const
     {
-        const int full = take / w;
-        if (k <= full) return 2 * chunk_tiles_prefix(base(), w, k);
-        const int rest = take - full * w;
+        const int full = take >> ws;
+        if (k <= full) return 2 * chunk_tiles_prefix(base(), ws, k);
+        const int rest = take - (full << ws);
         const int keys = base() + take;
-        const long long tiles = keys > 0 ? (keys + CH_KEYS - 1) / CH_KEYS : 0;
-        return 2 * chunk_tiles_prefix(base(), w, full) + (rest * g <= CH_ROWS / 2 ? 1 : 2) * tiles;
+        const long long tiles = keys > 0 ? (keys + CH_KEYS - 1) >> 7 : 0;
+        return 2 * chunk_tiles_prefix(base(), ws, full) + (2 * rest <= (1 << ws) ? 1 : 2) * tiles;
     }
-    __host__ __device__ int blocks(int w) const { return (take + w - 1) / w; }
+    __host__ __device__ int blocks(int ws) const { return static_cast<int>((static_cast<long long>(take) + (1 << ws) - 1) >> ws); }
 };
+
+// floor(a / b) for quotients below 2^20, a < 2^62: a float guess, which is off by at most one, put right.
+__host__ __device__ inline int small_quotient(long long a, long long b)
+{
+    int q = static_cast<int>(static_cast<float>(a) / static_cast<float>(b));
+    if (static_cast<long long>(q + 1) * b <= a) ++q;
+    if (static_cast<long long>(q) * b > a) --q;
+    return q;
+}
 
 // One unit: a block of query rows of one sequence and KV head.
 struct ChunkUnit {
@@ -73,7 +83,7 @@ struct ChunkPlan {
     const int* cu;
     const int* len;
     const long long* U;  // [B + 1]
-    int B, Hk, g, w, max_q;
+    int B, Hk, g, ws, max_q;  // blocks of 1 << ws tokens
     const PagedBatch* p;
 
     __host__ __device__ ChunkSeq seq(int b) const
@@ -85,13 +95,13 @@ struct ChunkPlan {
 
     __host__ __device__ void fill(ChunkUnit& u) const  // rows, keys and tiles from b, rb
     {
-        const int i0 = u.rb * w, left = min(u.s.take - i0, w);
+        const int w = 1 << ws, i0 = u.rb << ws, left = min(u.s.take - i0, w);
         u.rows = left * g;
         u.keys = max(u.s.base() + i0 + left, 0);
-        u.tiles = (u.keys + CH_KEYS - 1) / CH_KEYS;
+        u.tiles = (u.keys + CH_KEYS - 1) >> 7;
         u.cost = u.rows <= CH_ROWS / 2 ? 1 : 2;
         // the first 128 rows end with token i0 + w / 2 - 1 (g <= 64: w / 2 >= 2); g = 1: w = 256
-        u.tiles0 = u.cost == 1 ? u.tiles : (max(u.s.base() + i0 + w / 2, 0) + CH_KEYS - 1) / CH_KEYS;
+        u.tiles0 = u.cost == 1 ? u.tiles : (max(u.s.base() + i0 + w / 2, 0) + CH_KEYS - 1) >> 7;
     }
 
     // the unit holding point x (0 <= x < total())
@@ -108,16 +118,16 @@ struct ChunkPlan {
         u.s = seq(lo);
         const long long per = U[lo + 1] - U[lo];
         x -= U[lo] * Hk;
-        u.kvh = static_cast<int>(x / per);
+        u.kvh = small_quotient(x, per);
         x -= u.kvh * per;
-        int a = 0, z = u.s.blocks(w) - 1;
+        int a = 0, z = u.s.blocks(ws) - 1;
         while (a < z) {
             const int mid = (a + z + 1) >> 1;
-            if (u.s.cost(mid, w, g) <= x) a = mid;
+            if (u.s.cost(mid, ws) <= x) a = mid;
             else z = mid - 1;
         }
         u.rb = a;
-        u.U = U[lo] * Hk + u.kvh * per + u.s.cost(a, w, g);
+        u.U = U[lo] * Hk + u.kvh * per + u.s.cost(a, ws);
         fill(u);
         return u;
     }
@@ -128,7 +138,7 @@ struct ChunkPlan {
         u.U += static_cast<long long>(u.cost) * u.tiles;
         ++u.rb;
         while (u.b < B) {
-            const int nb = u.s.blocks(w);
+            const int nb = u.s.blocks(ws);
             for (; u.rb < nb; ++u.rb) {
                 fill(u);
                 if (u.tiles > 0) return;
@@ -146,8 +156,8 @@ struct ChunkPlan {
     __host__ __device__ bool piece(const ChunkUnit& u, long long lo, long long hi, int& tb, int& te) const
     {
         const long long a = max(lo, u.U) - u.U, z = min(hi - u.U, static_cast<long long>(u.cost) * u.tiles);
-        tb = static_cast<int>((a + u.cost - 1) / u.cost);
-        te = static_cast<int>((z + u.cost - 1) / u.cost);
+        tb = static_cast<int>((a + u.cost - 1) >> (u.cost - 1));
+        te = static_cast<int>((z + u.cost - 1) >> (u.cost - 1));
         return tb < te;
     }
 };
@@ -155,16 +165,21 @@ struct ChunkPlan {
 __host__ __device__ __forceinline__ int chunk_owner(long long x, long long N, int G)
 {
     // c with ceil(c N / G) <= x < ceil((c + 1) N / G)
-    return static_cast<int>((x * G) / N);
+    return small_quotient(x * G, N);
 }
 
 __host__ __device__ __forceinline__ long long chunk_start(int c, long long N, int G)
 {
-    return (static_cast<long long>(c) * N + G - 1) / G;
+    // ceil(c N / G): a guess in double, put right
+    const long long a = static_cast<long long>(c) * N;
+    long long q = static_cast<long long>(static_cast<double>(a) * (1.0 / G));
+    while (q * G < a) ++q;
+    while ((q - 1) * G >= a) --q;
+    return q;
 }
 
 // Block-wide: reads the batch, checks it, and builds the line's prefix.
-__device__ inline void chunk_plan_build(const PagedBatch& p, int Hk, int g, int max_q, int* s_cu, int* s_len,
+__device__ inline void chunk_plan_build(const PagedBatch& p, int ws, int max_q, int* s_cu, int* s_len,
                                         long long* s_U, bool report)
 {
     for (int b = threadIdx.x; b <= p.B; b += blockDim.x) {
@@ -172,16 +187,15 @@ __device__ inline void chunk_plan_build(const PagedBatch& p, int Hk, int g, int 
         if (b < p.B) s_len[b] = p.seq_lens[b];
     }
     __syncthreads();
-    const int w = CH_ROWS / g;
     for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
         const PagedSeq s = paged_seq(p, s_cu[b], s_cu[b + 1], s_len[b]);
         if (report && (s.bad || s.n > max_q)) report_status(p.dev_status, KVATTN_STATUS_BAD_LENGTH);
         const ChunkSeq q{s.t0, s.n, min(s.n, max_q), s.len};
-        s_U[b + 1] = q.cost(q.blocks(w), w, g);
+        s_U[b + 1] = q.cost(q.blocks(ws), ws);
     }
     if (threadIdx.x == 0) s_U[0] = 0;
     __syncthreads();
-    if (threadIdx.x < 32) {
+    if (threadIdx.x < 32 && p.B > 1) {
         const int lane = threadIdx.x;
         const int per = (p.B + 31) / 32;
         const int beg = min(lane * per, p.B), end = min(beg + per, p.B);

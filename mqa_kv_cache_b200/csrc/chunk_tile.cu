@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
     const int w = CH_ROWS / a.g;
     int gs = 0;
     while ((1 << gs) < a.g) ++gs;
-    chunk_plan_build(p, a.Hk, a.g, a.max_q, s_cu, s_len, s_U, blockIdx.x == 0);
-    const ChunkPlan plan{s_cu, s_len, s_U, p.B, a.Hk, a.g, w, a.max_q, &p};
+    chunk_plan_build(p, 8 - gs, a.max_q, s_cu, s_len, s_U, blockIdx.x == 0);
+    const ChunkPlan plan{s_cu, s_len, s_U, p.B, a.Hk, a.g, 8 - gs, a.max_q, &p};
     // tokens that stand before row 0 see nothing (their blocks may have no unit)
     bool any_blind = false;
     for (int b = threadIdx.x; b < p.B; b += blockDim.x) any_blind |= plan.seq(b).base() < 0;
@@ -516,13 +516,14 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         uint32_t it0 = 0;   // first tile number of the piece
         uint32_t cnt = 0;   // tiles of this buffer so far
         uint32_t joins = 0;
-        Piece u;
-        for (int n = 0; take(n, u); ++n) {
+        for (int n = 0;; ++n) {
+            // the piece stays in shared memory, and is read where it is needed: registers are short here
+            if (!ready(&piece_full[n % PIECES], (n / PIECES) & 1, s_abort)) break;
+            const volatile Piece& u = s_piece[n % PIECES];
+            if (u.rows == 0) break;
             const int tb = u.tb, te = u.te;
             const bool pair = u.cost == 2;  // two Q tiles; else one, its key tiles dealt out in turn
             const int row0 = (pair ? t * 128 : 0) + r16;  // the warp's first row of the block
-            const int rowa = row0 + (lane >> 2), rowb = rowa + 8;
-            const int posa = u.pos0 + (rowa >> gs), posb = u.pos0 + (rowb >> gs);
             const int pos_first = u.pos0 + (row0 >> gs);
             const bool active_warp = row0 < u.rows;
             const int n_my = pair ? max((t == 0 ? min(te, u.tiles0) : te) - tb, 0) : (te - tb + 1 - t) / 2;
@@ -577,7 +578,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                         }
                     }
                     if (masked) {
-                        const int lima = posa - j * CH_KEYS, limb = posb - j * CH_KEYS;  // keys 0 .. lim of the tile are seen
+                        // keys 0 .. lim of the tile are seen
+                        const int pos0 = u.pos0 - j * CH_KEYS, ra = row0 + (lane >> 2);
+                        const int lima = pos0 + (ra >> gs), limb = pos0 + ((ra + 8) >> gs);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             uint32_t* x = sv[i >> 3] + 4 * (i & 7);
@@ -698,6 +701,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 c1 = c0 + D / 32;
             }
             const bool whole = u.count == 1;
+            const int rowa = row0 + (lane >> 2), rowb = rowa + 8, rows = u.rows;
             if (whole) {
                 const float ia = la > 0.f ? 1.f / la : 0.f, ib = lb > 0.f ? 1.f / lb : 0.f;
                 ua *= ia;
@@ -709,32 +713,26 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             const long long outa = base + static_cast<long long>(rowa >> gs) * a.H + (rowa & (a.g - 1));
             const long long outb = base + static_cast<long long>(rowb >> gs) * a.H + (rowb & (a.g - 1));
             const long long part = static_cast<long long>(2 * c + u.first) * CH_ROWS;
-            const bool usea = ok && rowa < u.rows, useb = ok && rowb < u.rows;
+            const bool usea = ok && rowa < rows, useb = ok && rowb < rows;
+            constexpr int EC = 16;  // columns at a time (more cost registers that the tile loop needs)
 #pragma unroll 1
             for (int cc = c0; cc < c1; ++cc) {
-                uint32_t ov[8];
-                tmem_ld_16x256b_x2(o_base + t * D + cc * 16, ov);
+                uint32_t ov[EC / 2], ow[EC / 2];
+                tmem_ld_16x256b_x2(o_base + t * D + cc * EC, ov);
+                if (!pair) tmem_ld_16x256b_x2(o_base + (t ^ 1) * D + cc * EC, ow);
                 tmem_wait_ld();
                 tmem_regs_ready(ov);
-                float x[8];
+                if (!pair) tmem_regs_ready(ow);
+                float x[EC / 2];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float f = (i & 2) ? ub : ua;
+                for (int i = 0; i < EC / 2; ++i) {
+                    const float f = (i & 2) ? ub : ua, h = (i & 2) ? vb : va;
                     x[i] = f == 0.f ? 0.f : __uint_as_float(ov[i]) * f;
-                }
-                if (!pair) {
-                    tmem_ld_16x256b_x2(o_base + (t ^ 1) * D + cc * 16, ov);
-                    tmem_wait_ld();
-                    tmem_regs_ready(ov);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float f = (i & 2) ? vb : va;
-                        if (f != 0.f) x[i] = fmaf(__uint_as_float(ov[i]), f, x[i]);
-                    }
+                    if (!pair && h != 0.f) x[i] = fmaf(__uint_as_float(ow[i]), h, x[i]);
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int col = cc * 16 + 8 * i + q2;
+                for (int i = 0; i < EC / 8; ++i) {
+                    const int col = cc * EC + 8 * i + q2;
                     if (whole) {
                         if (usea) *reinterpret_cast<uint32_t*>(a.out + outa * D + col) = pack_bf16x2(x[4 * i], x[4 * i + 1]);
                         if (useb) *reinterpret_cast<uint32_t*>(a.out + outb * D + col) = pack_bf16x2(x[4 * i + 2], x[4 * i + 3]);
@@ -755,8 +753,9 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             }
             // the other group reads this buffer's accumulator: the next piece waits for it
             tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&piece_empty[n % PIECES]);
             if (!pair) {
-                __syncwarp();
                 if (lane == 0) mbar_arrive(&joined[1]);
                 ready(&joined[1], joins & 1, s_abort);
                 ++joins;
@@ -782,7 +781,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 ok = ready(q_full, n & 1, s_abort);
                 if (!ok) break;
 #pragma unroll 2
-                for (int i = 0; i < u.cost * 128 * (D / 8) / 128; ++i) {
+                for (int i = 0; i < u.cost * (D / 8); ++i) {
                     const int id = i * 128 + tid, row = id / (D / 8), c8 = id % (D / 8);
                     uint4* q = reinterpret_cast<uint4*>(smem + C::OFF_Q + (row >> 7) * C::TILE + (c8 >> 3) * C::BOX + swz128(row & 127, c8 & 7));
                     const uint4 v = *q;
@@ -792,16 +791,17 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     for (int e = 0; e < 4; ++e) m = fmax3(m, fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e])));
 #pragma unroll
                     for (int o = D / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    // largest element to [2^14, 2^15): an element below 2^-29 of it rounds to a multiple of 2^-40 of
-                    // it, far below the fp32 sums' own rounding; two factors, as one may leave fp32's range
-                    const int ex = m > 0.f ? 14 - ilogbf(m) : 0;
-                    const float fa = ldexpf(1.f, ex / 2), fb = ldexpf(1.f, ex - ex / 2);
+                    // largest element to [2^14, 2^15), by its exponent field (0 of a zero or subnormal row: taken as
+                    // 1): an element below 2^-29 of the largest rounds to a multiple of 2^-40 of it, far below the
+                    // fp32 sums' own rounding.  Two factors, as one may leave fp32's range: 2^(141 - e) = fa fb.
+                    const int e8 = max(static_cast<int>(__float_as_uint(m) >> 23), 1), up = 141 - e8;
+                    const float fa = __int_as_float((127 + (up >> 1)) << 23), fb = __int_as_float((127 + up - (up >> 1)) << 23);
                     uint32_t o[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[e]) : "f"(bf16_hi(w[e]) * fa * fb), "f"(bf16_lo(w[e]) * fa * fb));
                     *q = make_uint4(o[0], o[1], o[2], o[3]);
-                    if (c8 == 0) s_qs[(n & 1) * CH_ROWS + row] = ldexpf(1.f, -ex);
+                    if (c8 == 0) s_qs[(n & 1) * CH_ROWS + row] = __int_as_float((127 - (up >> 1)) << 23) * __int_as_float((127 - up + (up >> 1)) << 23);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         if (lane == 0) {
             const long long N = plan.total();
             // every CTA's stretch holds two points at least, so that it owns a tile of each unit it lies in
-            const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), N / 2 > 0 ? N / 2 : 1));
+            const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), N > 2 ? N >> 1 : 1));
             int4 split = make_int4(0, 0, 0, 0);
             int np = 0;
             bool ok = true;
@@ -914,6 +914,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
 // out = sum w_i O_i / sum w_i l_i and lse = ln 2 (M + log2 sum w_i l_i), in the
 // partials' order.
 constexpr int TM_WARPS = 8;
+constexpr int TM_BLOCKS = 16;  // per unit: 32 rows a pass.  (4 blocks: splits over many CTAs took twice as long.)
 
 template <int D>
 __global__ void __launch_bounds__(TM_WARPS * 32) chunk_tile_merge_kernel(ChunkArgs a)
@@ -924,43 +925,44 @@ __global__ void __launch_bounds__(TM_WARPS * 32) chunk_tile_merge_kernel(ChunkAr
     const int f = blockIdx.x;
     const int4 info = a.split_info[f];
     const int lane = threadIdx.x & 31;
-    const int row = blockIdx.y * TM_WARPS + (threadIdx.x >> 5);
-    if (row >= info.y || info.w < 2) return;
     const int count = info.w;
-    float M = -INFINITY;
-    for (int i = lane; i < count; i += 32)
-        M = fmaxf(M, a.part_ml[static_cast<long long>(i == 0 ? 2 * f + 1 : 2 * (f + i)) * CH_ROWS + row].x);
+    if (count < 2) return;
+    for (int row = blockIdx.y * TM_WARPS + (threadIdx.x >> 5); row < info.y; row += TM_WARPS * TM_BLOCKS) {
+        float M = -INFINITY;
+        for (int i = lane; i < count; i += 32)
+            M = fmaxf(M, a.part_ml[static_cast<long long>(i == 0 ? 2 * f + 1 : 2 * (f + i)) * CH_ROWS + row].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float mu = M == -INFINITY ? 0.f : M;
-    float L = 0.f, acc[PL];
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float mu = M == -INFINITY ? 0.f : M;
+        float L = 0.f, acc[PL];
 #pragma unroll
-    for (int i = 0; i < PL; ++i) acc[i] = 0.f;
+        for (int i = 0; i < PL; ++i) acc[i] = 0.f;
 #pragma unroll 4
-    for (int i = 0; i < count; ++i) {
-        const long long pr = static_cast<long long>(i == 0 ? 2 * f + 1 : 2 * (f + i)) * CH_ROWS + row;
-        const float2 ml = a.part_ml[pr];
-        const float wi = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mu);
-        L += wi * ml.y;
-        const float* o = a.part_o + pr * D + lane * PL;
-        if constexpr (PL == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(o);
-            acc[0] += wi * v.x;
-            acc[1] += wi * v.y;
-            acc[PL - 2] += wi * v.z;
-            acc[PL - 1] += wi * v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(o);
-            acc[0] += wi * v.x;
-            acc[1] += wi * v.y;
+        for (int i = 0; i < count; ++i) {
+            const long long pr = static_cast<long long>(i == 0 ? 2 * f + 1 : 2 * (f + i)) * CH_ROWS + row;
+            const float2 ml = a.part_ml[pr];
+            const float wi = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mu);
+            L += wi * ml.y;
+            const float* o = a.part_o + pr * D + lane * PL;
+            if constexpr (PL == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(o);
+                acc[0] += wi * v.x;
+                acc[1] += wi * v.y;
+                acc[PL - 2] += wi * v.z;
+                acc[PL - 1] += wi * v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(o);
+                acc[0] += wi * v.x;
+                acc[1] += wi * v.y;
+            }
         }
-    }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    const long long orow = (static_cast<long long>(info.x) + row / a.g) * a.H + static_cast<long long>(info.z) * a.g + row % a.g;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * PL);
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const long long orow = (static_cast<long long>(info.x) + row / a.g) * a.H + static_cast<long long>(info.z) * a.g + row % a.g;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * PL);
 #pragma unroll
-    for (int i = 0; i < PL; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+        for (int i = 0; i < PL; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+        if (lane == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+    }
 }
 
 template <int D, bool FP8>
@@ -980,7 +982,7 @@ cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& tm_q, const CUte
     e = launch_pdl(chunk_tile_kernel<D, FP8>, dim3(grid), dim3(TCfg<D, FP8>::THREADS), TCfg<D, FP8>::SMEM, stream, tm_q,
                    tm_k, tm_v, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(chunk_tile_merge_kernel<D>, dim3(grid, CH_ROWS / TM_WARPS), dim3(TM_WARPS * 32), 0, stream, a);
+    return launch_pdl(chunk_tile_merge_kernel<D>, dim3(grid, TM_BLOCKS), dim3(TM_WARPS * 32), 0, stream, a);
 }
 
 }  // namespace
