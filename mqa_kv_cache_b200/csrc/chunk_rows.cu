@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
     using C = RCfg<D, FP8, NQ, NMT>;
     constexpr int KS = D / 16, STAGES = C::STAGES, RM = C::RM, RW = C::RW, WR = C::WR;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (stays a shared-memory address to the compiler)
     float* s_o = reinterpret_cast<float*>(smem + C::OFF_O);
     float2* s_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
     long long* s_U = reinterpret_cast<long long*>(smem + C::OFF_U);

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
     using C = TCfg<D, FP8>;
     constexpr int NS = C::NS, LS = C::LS;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (stays a shared-memory address to the compiler)
     uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* kv_empty = kv_full + NS;
     uint64_t* land_full = kv_empty + NS;
