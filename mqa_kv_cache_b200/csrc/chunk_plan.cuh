@@ -73,7 +73,7 @@ struct ChunkUnit {
     int rows;        // query rows in use
     int keys;        // keys that its last token sees
     int tiles;       // 128-key tiles of them
-    int tiles0;      // tiles that the first 128 rows see
+    int keys0;       // keys that the last token of the first 128 rows sees
     int cost;        // points per tile
 };
 
@@ -101,7 +101,7 @@ struct ChunkPlan {
         u.tiles = (u.keys + CH_KEYS - 1) >> 7;
         u.cost = u.rows <= CH_ROWS / 2 ? 1 : 2;
         // the first 128 rows end with token i0 + w / 2 - 1 (g <= 64: w / 2 >= 2); g = 1: w = 256
-        u.tiles0 = u.cost == 1 ? u.tiles : (max(u.s.base() + i0 + w / 2, 0) + CH_KEYS - 1) >> 7;
+        u.keys0 = u.cost == 1 ? u.keys : max(u.s.base() + i0 + w / 2, 0);
     }
 
     // the unit holding point x (0 <= x < total())

@@ -10,17 +10,20 @@
 // Work: chunk_plan.cuh.  A persistent CTA walks its stretch of (block, key tile)s.  A
 // block of more than 128 rows is two Q tiles that share every K/V tile, so that the
 // softmax of one overlaps the products of the other; a block of at most 128 rows is one
-// Q tile whose even and odd key tiles go to the two softmax groups, each with its own
-// maximum, sum and accumulator, joined from tensor memory at the end.
+// Q tile whose key tiles' halves go to the two softmax groups, each with its own maximum,
+// sum and accumulator, joined from tensor memory at the end.
 //
 // Warps: 0-7 / 8-15 softmax of the two buffers (16 rows a warp, 64 scores a thread: half the
 // time of a thread per row, which the chain scores - softmax - P V - next scores waits for),
-// 16 issues the MMAs, 17 loads K/V pages (one box per page and 64-column half, page entries
-// fetched one tile ahead), 18 loads Q, 19 hands out the pieces.  FP8: warps 20-23 turn the
+// 16 issues the scores' MMAs, 18 the values', 17 loads K/V pages (one box per page and
+// 64-column half, page entries fetched one tile ahead), 19 hands out the pieces and loads Q.  FP8: warps 20-23 turn the
 // codes of each landed tile into bf16 (exact) in the layout that the MMAs read; the keys'
 // scales multiply the scores and the values' scales the weights, in fp32.
-// TMEM: S0 | S1 | O0 | O1; the weights (bf16) overwrite the first half of their scores
-// and the P V product takes them from there.
+// TMEM: S0 | S1 | O0 | O1.  Scores are computed 64 keys at a time in either half of their 128
+// columns, one step ahead of the softmax; the weights (bf16) overwrite the first half of
+// their scores and the P V product takes them from there.  (128 keys at a time, where the
+// next scores wait for the P V that reads the weights in their place, the chain scores -
+// softmax - P V took 3960 cycles a tile against 2050 of the products alone.)
 #include "chunk_plan.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -40,12 +43,24 @@ struct Piece {
     int pos0;    // its position
     int rows, keys;
     int tb, te;  // tiles
-    int tiles0;  // tiles that the first 128 rows see
+    int keys0;   // keys that the first 128 rows see
     int cost;    // 2: two Q tiles, 1: one
     int count;   // pieces of the unit
     int first;   // whether this is the first of them
 };
 constexpr int PIECES = 4;
+constexpr int CH_STEP = 64;  // keys whose scores are computed at a time
+
+// Steps of a piece that buffer t takes.  Two Q tiles (buffer = tile): the steps of its tiles that its rows see.
+// One: the halves of each tile go to the two buffers, so the last step may be buffer 0's alone.
+template <typename P>
+__device__ __forceinline__ int piece_steps(const P& u, int t)
+{
+    const int tiles = u.te - u.tb;
+    auto upto = [&](int keys) { return max(min(2 * tiles, ((keys + CH_STEP - 1) >> 6) - 2 * u.tb), 0); };
+    if (u.cost == 2) return upto(t ? u.keys : u.keys0);
+    return (upto(u.keys) + 1 - t) >> 1;
+}
 
 template <int D, bool FP8>
 struct TCfg {
@@ -68,16 +83,16 @@ struct TCfg {
     static constexpr int OFF_QS = OFF_ML + 2 * 128 * 8;  // [2 pieces][256] powers of two that Q's rows were divided by (FP8)
     static constexpr int OFF_PIECE = OFF_QS + (FP8 ? 2 * CH_ROWS * 4 : 0);
     static constexpr int OFF_BAR = OFF_PIECE + PIECES * static_cast<int>(sizeof(Piece));
-    // kv_full[NS], kv_empty[NS], land_full[LS], land_empty[LS], q_full, q_empty, s_full[2], p_full[2], pv_done[2],
+    // kv_full[NS], kv_empty[NS], land_full[LS], land_empty[LS], q_full, q_empty, s_full[4], p_full[4], pv_done[4],
     // joined[2], piece_full[PIECES], piece_empty[PIECES], done, q_ready
-    static constexpr int NBAR = 2 * NS + 2 * LS + 12 + 2 * PIECES;
-    // warps that take every piece: 16 of the softmax, MMA, K/V loads, Q loads, 4 of the widening
+    static constexpr int NBAR = 2 * NS + 2 * LS + 18 + 2 * PIECES;
+    // warps that take every piece: 16 of the softmax, both MMA warps, K/V loads, 4 of the widening
     static constexpr int TAKERS = FP8 ? 23 : 19;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + RING * 4 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
     // Q x K in bf16, or in fp16 with FP8 (formats 0 instead of 1 in bits 7 and 10)
-    static constexpr uint32_t IDESC_S = umma_idesc_bf16(128, CH_KEYS) & (FP8 ? ~((1u << 7) | (1u << 10)) : ~0u);
+    static constexpr uint32_t IDESC_S = umma_idesc_bf16(128, CH_STEP) & (FP8 ? ~((1u << 7) | (1u << 10)) : ~0u);
     static constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D, false, true);
 };
 
@@ -204,10 +219,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
     uint64_t* q_full = land_empty + LS;
     uint64_t* q_empty = q_full + 1;
     uint64_t* s_full = q_full + 2;
-    uint64_t* p_full = q_full + 4;
-    uint64_t* pv_done = q_full + 6;
-    uint64_t* joined = q_full + 8;
-    uint64_t* piece_full = q_full + 10;
+    uint64_t* p_full = q_full + 6;   // (each: buffer t, half h at 2 t + h)
+    uint64_t* pv_done = q_full + 10;
+    uint64_t* joined = q_full + 14;
+    uint64_t* piece_full = q_full + 16;
     uint64_t* piece_empty = piece_full + PIECES;
     uint64_t* done = piece_empty + PIECES;
     uint64_t* q_ready = done + 1;  // FP8: Q's rows are fp16
@@ -234,17 +249,17 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 2);  // the products' commit, and their issuer
             mbar_init(&p_full[i], 8);
             mbar_init(&pv_done[i], 1);
-            mbar_init(&joined[i], 16);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(&joined[i], 16);
         for (int i = 0; i < PIECES; ++i) {
             mbar_init(&piece_full[i], 1);
             mbar_init(&piece_empty[i], C::TAKERS);
         }
-        mbar_init(done, 1);
+        mbar_init(done, 2);
         mbar_init(q_ready, 4);
         *s_abort = 0;
         fence_barrier_init();
@@ -286,20 +301,13 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         }
     }
     const int c = blockIdx.x;
-    // piece i of this CTA, for a whole warp / for one thread; false: none left (or a wait ran out)
+    // piece i of this CTA, for a whole warp; false: none left (or a wait ran out)
     auto take = [&](int i, Piece& pc) {
         const int k = i % PIECES;
         if (!warp_wait(&piece_full[k], (i / PIECES) & 1, s_abort)) return false;
         pc = s_piece[k];
         __syncwarp();
         if (lane == 0) mbar_arrive(&piece_empty[k]);
-        return pc.rows > 0;
-    };
-    auto take1 = [&](int i, Piece& pc) {
-        const int k = i % PIECES;
-        if (*s_abort || !mbar_wait(&piece_full[k], (i / PIECES) & 1)) return false;
-        pc = s_piece[k];
-        mbar_arrive(&piece_empty[k]);
         return pc.rows > 0;
     };
 
@@ -381,131 +389,100 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             uint64_t* full = FP8 ? land_full : kv_full;
             for (uint32_t i = x > R ? x - R : 0; i < x; ++i) mbar_wait(&full[i % R], (i / R) & 1);
         }
-    } else if (warp == 18) {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
-        // ===== Q: [128 / g tokens][g heads] boxes, one or two tiles a piece =====
-        if (lane == 0) {
-            int np = 0;
-            Piece u;
-            while (take1(np, u)) {
-                if (np > 0 && (*s_abort || !mbar_wait(q_empty, (np - 1) & 1))) {
-                    *s_abort = 1;
-                    break;
-                }
-                mbar_arrive_expect_tx(q_full, u.cost * C::TILE);
-                for (int t = 0; t < u.cost; ++t)
-#pragma unroll
-                    for (int h = 0; h < C::HALVES; ++h)
-                        tma_load_3d(smem + C::OFF_Q + t * C::TILE + h * C::BOX, &tm_q, q_full, h * 64, u.kvh * a.g,
-                                    u.tok0 + t * (w / 2));
-                ++np;
-            }
-            if (np > 0) mbar_wait(q_full, (np - 1) & 1);
-        }
     } else if (warp == 16) {
         if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
-        // ===== MMA issue =====
-        {
-            const uint32_t el = elect_one();
-            const uint32_t sq = smem_u32(smem + C::OFF_Q), skv = smem_u32(smem + C::OFF_KV);
-            bool ok = true;
-            uint32_t x0 = 0;                  // first K/V tile number of the piece
-            uint32_t pv0 = 0, pv1 = 0;        // P V products issued to each buffer
-            int np = 0;
-            // scores of Q tile q in buffer t; the weights in its columns have been used by then
-            auto scores = [&](int t, int q, uint32_t x, bool landed = false) {
-                const uint32_t slot = x % NS;
-                ok = ok && (landed || ready(&kv_full[slot], (x / NS) & 1, s_abort));
-                const uint32_t pv = t ? pv1 : pv0;
-                if (ok && pv) ok = ready(&pv_done[t], (pv - 1) & 1, s_abort);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t d = tmem + t * CH_KEYS, qa = sq + q * C::TILE, ka = skv + slot * C::TILE;
+        // ===== scores: S_t = Q K^T, a step ahead of the softmax (while that works on step i, step i + 1 is
+        // multiplied), into half g % 2 of buffer t for its step number g =====
+        const uint32_t el = elect_one();
+        const uint32_t sq = smem_u32(smem + C::OFF_Q), skv = smem_u32(smem + C::OFF_KV);
+        bool ok = true;
+        uint32_t x0 = 0;            // first K/V tile number of the piece
+        uint32_t gn[2] = {0, 0};    // steps so far, per buffer
+        Piece u;
+        for (int np = 0; ok && take(np, u); ++np) {
+            ok = ready(FP8 ? q_ready : q_full, np & 1, s_abort);
+            const bool pair = u.cost == 2;
+            const int n0 = piece_steps(u, 0), n1 = piece_steps(u, 1), n = max(n0, n1);
+#pragma unroll 1
+            for (int i = 0; i < n && ok; ++i) {
+                const uint32_t x = x0 + 2 * (pair ? i >> 1 : i), slot = x % NS;
+                // (of a tile's steps, the first one waits for it)
+                if (!pair || !(i & 1)) ok = ready(&kv_full[slot], (x / NS) & 1, s_abort);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * C::BOX + (ks & 3) * 32;
-                    mma_ss(el, d, umma_desc_k_sw128(qa + off), umma_desc_k_sw128(ka + off), C::IDESC_S, ks > 0 ? 1u : 0u);
-                }
-                commit_to(el, &s_full[t]);
-                if (el) mbar_arrive(&s_full[t]);
-            };
-            auto values = [&](int t, bool acc, uint32_t x, bool landed = false) {
-                const uint32_t slot = x % NS;
-                ok = ok && (landed || ready(&kv_full[slot], (x / NS) & 1, s_abort));
-                if (ok) ok = ready(&p_full[t], (t ? pv1 : pv0) & 1, s_abort);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t va = skv + slot * C::TILE;
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t g = gn[t];
+                    if (!ok || i >= (t ? n1 : n0)) continue;
+                    // the weights that stand in the place have been used
+                    if (g >= 2 && !(ok = ready(&pv_done[2 * t + (g & 1)], ((g >> 1) - 1) & 1, s_abort))) continue;
+                    tc_fence_after();
+                    const uint32_t d = tmem + t * CH_KEYS + (g & 1) * CH_STEP;
+                    const uint32_t qa = sq + (pair ? t * C::TILE : 0);
+                    const uint32_t ka = skv + slot * C::TILE + (pair ? i & 1 : t) * (CH_STEP * 128);
 #pragma unroll
-                for (int ks = 0; ks < CH_KEYS / 16; ++ks)
-                    mma_ts(el, tmem + 256 + t * D, tmem + t * CH_KEYS + ks * 8,
-                                   umma_desc_mn_sw128(va + ks * 2048, C::BOX, 1024), C::IDESC_O, (acc || ks > 0) ? 1u : 0u);
-                commit_to(el, &pv_done[t]);
-                if (t) ++pv1;
-                else ++pv0;
-            };
-            Piece u;
-            while (ok && take(np, u)) {
-                const int tb = u.tb, te = u.te;
-                ok = ready(FP8 ? q_ready : q_full, np & 1, s_abort);
-                ++np;
-                if (!ok) break;
-                const int n = te - tb;
-                if (u.cost == 2) {
-                    const int n0 = min(te, u.tiles0) - tb;  // tiles of Q tile 0 (it may see none of these)
-                    if (n0 > 0) scores(0, 0, x0);
-                    scores(1, 1, x0, n0 > 0);
-                    if (ok) commit_to(el, &kv_empty[x0 % NS]);
-                    if (ok && n == 1) commit_to(el, q_empty);
-                    // each Q tile's P V, then at once its next scores
-                    for (int k = 0; k < n && ok; ++k) {
-                        const uint32_t xv = x0 + 2 * k + 1, xk = xv + 1;
-                        if (k < n0) values(0, k > 0, xv);
-                        if (k + 1 < n0) scores(0, 0, xk);
-                        values(1, k > 0, xv, k < n0);
-                        if (ok) commit_to(el, &kv_empty[xv % NS]);
-                        if (k + 1 < n) {
-                            scores(1, 1, xk, k + 1 < n0);
-                            if (ok) commit_to(el, &kv_empty[xk % NS]);
-                            if (ok && k + 2 == n) commit_to(el, q_empty);
-                        }
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * C::BOX + (ks & 3) * 32;
+                        mma_ss(el, d, umma_desc_k_sw128(qa + off), umma_desc_k_sw128(ka + off), C::IDESC_S, ks > 0 ? 1u : 0u);
                     }
-                } else {
-                    // one Q tile: even tiles in buffer 0, odd ones in buffer 1
-                    scores(0, 0, x0);
-                    if (ok) commit_to(el, &kv_empty[x0 % NS]);
-                    if (n > 1) {
-                        scores(1, 0, x0 + 2);
-                        if (ok) commit_to(el, &kv_empty[(x0 + 2) % NS]);
-                    }
-                    if (ok && n <= 2) commit_to(el, q_empty);
-                    for (int k = 0; k < n && ok; ++k) {
-                        const int t = k & 1;
-                        values(t, k > 1, x0 + 2 * k + 1);
-                        if (ok) commit_to(el, &kv_empty[(x0 + 2 * k + 1) % NS]);
-                        if (k + 2 < n) {
-                            scores(t, 0, x0 + 2 * k + 4);
-                            if (ok) commit_to(el, &kv_empty[(x0 + 2 * k + 4) % NS]);
-                            if (ok && k + 3 == n) commit_to(el, q_empty);
-                        }
-                    }
+                    commit_to(el, &s_full[2 * t + (g & 1)]);
+                    if (el) mbar_arrive(&s_full[2 * t + (g & 1)]);
+                    ++gn[t];
                 }
-                x0 += 2 * n;
+                if (ok && (!pair || (i & 1) || i + 1 == n)) commit_to(el, &kv_empty[slot]);
             }
-            if (*s_abort && el) report_status(p.dev_status, KVATTN_STATUS_TIMEOUT);
-            commit_to(el, done);
-            mbar_wait(done, 0);
-            __syncwarp();
+            if (ok) commit_to(el, q_empty);
+            x0 += 2 * (u.te - u.tb);
         }
+        if (*s_abort && el) report_status(p.dev_status, KVATTN_STATUS_TIMEOUT);
+        commit_to(el, done);
+        mbar_wait(done, 0);
+        __syncwarp();
+    } else if (warp == 18) {
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+        // ===== O_t += P V, step by step =====
+        const uint32_t el = elect_one();
+        const uint32_t skv = smem_u32(smem + C::OFF_KV);
+        bool ok = true;
+        uint32_t x0 = 1;
+        uint32_t gn[2] = {0, 0};
+        Piece u;
+        for (int np = 0; ok && take(np, u); ++np) {
+            const bool pair = u.cost == 2;
+            const int n0 = piece_steps(u, 0), n1 = piece_steps(u, 1), n = max(n0, n1);
+#pragma unroll 1
+            for (int i = 0; i < n && ok; ++i) {
+                const uint32_t x = x0 + 2 * (pair ? i >> 1 : i), slot = x % NS;
+                if (!pair || !(i & 1)) ok = ready(&kv_full[slot], (x / NS) & 1, s_abort);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t g = gn[t];
+                    if (!ok || i >= (t ? n1 : n0) || !(ok = ready(&p_full[2 * t + (g & 1)], (g >> 1) & 1, s_abort))) continue;
+                    tc_fence_after();
+                    const uint32_t va = skv + slot * C::TILE + (pair ? i & 1 : t) * (CH_STEP * 128);
+                    const uint32_t pa = tmem + t * CH_KEYS + (g & 1) * CH_STEP;
+#pragma unroll
+                    for (int ks = 0; ks < CH_STEP / 16; ++ks)
+                        mma_ts(el, tmem + 256 + t * D, pa + ks * 8, umma_desc_mn_sw128(va + ks * 2048, C::BOX, 1024),
+                               C::IDESC_O, (i > 0 || ks > 0) ? 1u : 0u);
+                    commit_to(el, &pv_done[2 * t + (g & 1)]);
+                    ++gn[t];
+                }
+                if (ok && (!pair || (i & 1) || i + 1 == n)) commit_to(el, &kv_empty[slot]);
+            }
+            x0 += 2 * (u.te - u.tb);
+        }
+        if (*s_abort && el) report_status(p.dev_status, KVATTN_STATUS_TIMEOUT);
+        commit_to(el, done);
+        mbar_wait(done, 0);
+        __syncwarp();
     } else if (warp < 16) {
         // registers: 640 threads at 96 = 512 x 104 + 128 x 64; with FP8 768 at 80 = 512 x 96 + 128 x 40 + 128 x 56
         if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;" ::: "memory");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
         // ===== softmax + epilogue: warps 0-7 buffer 0, warps 8-15 buffer 1, 16 rows each =====
         // A row's scores are spread over a lane quad: thread (g, q) = (lane / 4, lane % 4) holds, of rows g and
-        // g + 8 of the warp's 16, the keys 8 j + 2 q and 8 j + 2 q + 1.
+        // g + 8 of the warp's 16, the keys 8 j + 2 q and 8 j + 2 q + 1 of a step of 64.
         const int t = warp >> 3, quarter = warp & 3, half = (warp >> 2) & 1;
         const int r16 = quarter * 32 + half * 16;  // the warp's first row of the Q tile = TMEM lane
         const int q2 = 2 * (lane & 3);
@@ -514,38 +491,39 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         const uint32_t o_base = tmem + lane_off + 256;
         const float sl2 = a.scale * kLog2e;
         uint32_t it0 = 0;   // first tile number of the piece
-        uint32_t cnt = 0;   // tiles of this buffer so far
+        uint32_t cnt = 0;   // steps of this buffer so far
         uint32_t joins = 0;
         for (int n = 0;; ++n) {
             // the piece stays in shared memory, and is read where it is needed: registers are short here
             if (!ready(&piece_full[n % PIECES], (n / PIECES) & 1, s_abort)) break;
             const volatile Piece& u = s_piece[n % PIECES];
             if (u.rows == 0) break;
-            const int tb = u.tb, te = u.te;
-            const bool pair = u.cost == 2;  // two Q tiles; else one, its key tiles dealt out in turn
+            const int tb = u.tb;
+            const bool pair = u.cost == 2;  // two Q tiles; else one, its keys dealt out in steps
             const int row0 = (pair ? t * 128 : 0) + r16;  // the warp's first row of the block
             const int pos_first = u.pos0 + (row0 >> gs);
             const bool active_warp = row0 < u.rows;
-            const int n_my = pair ? max((t == 0 ? min(te, u.tiles0) : te) - tb, 0) : (te - tb + 1 - t) / 2;
+            const int n_my = piece_steps(u, t);
             float sl2a = sl2, sl2b = sl2;  // raw scores to log2 units
             float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;  // maxima of the rows; this thread's share of their sums
             for (int k = 0; k < n_my; ++k, ++cnt) {
-                const int j = pair ? tb + k : tb + 2 * k + t;
-                const uint32_t it = it0 + (j - tb);
-                if (!ready(&s_full[t], cnt & 1, s_abort)) continue;
+                const int jt = pair ? k >> 1 : k, hh = pair ? k & 1 : t;  // tile of the piece, half of it
+                const int kb = (tb + jt) * CH_KEYS + hh * CH_STEP;         // first key of the step
+                const uint32_t it = it0 + jt;
+                const uint32_t sp = s_addr + (cnt & 1) * CH_STEP;
+                if (!ready(&s_full[2 * t + (cnt & 1)], (cnt >> 1) & 1, s_abort)) continue;
                 tc_fence_after();
-                const int nv = min(u.keys - j * CH_KEYS, CH_KEYS);
-                if (!FP8 && nv < CH_KEYS) {
+                if (!FP8 && u.keys - kb < CH_STEP) {
                     // rows of V behind the last key in use were not loaded, or hold what nobody may see:
                     // zeros, so that 0 * garbage cannot reach a sum (the P V waits for these warps)
                     const uint32_t xv = 2 * it + 1;
                     if (!ready(&kv_full[xv % NS], (xv / NS) & 1, s_abort)) continue;
-                    const int vr = (threadIdx.x & 255) >> 1;
-                    if (vr >= nv) {
-                        uint8_t* v = smem + C::OFF_KV + (xv % NS) * C::TILE + vr * 128 + (lane & 1) * 64;
+                    const int vr = (threadIdx.x & 255) >> 2;
+                    if (vr >= u.keys - kb) {
+                        uint8_t* v = smem + C::OFF_KV + (xv % NS) * C::TILE + (hh * CH_STEP + vr) * 128 + (lane & 3) * 32;
 #pragma unroll
-                        for (int i = 0; i < C::HALVES * 4; ++i)
-                            *reinterpret_cast<uint4*>(v + (i >> 2) * C::BOX + (i & 3) * 16) = make_uint4(0, 0, 0, 0);
+                        for (int i = 0; i < C::HALVES * 2; ++i)
+                            *reinterpret_cast<uint4*>(v + (i >> 1) * C::BOX + (i & 1) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
@@ -555,20 +533,18 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     sl2b = sl2 * qs[8];
                 }
                 if (active_warp) {
-                    const uint32_t bad = s_bad[it % C::RING];
-                    const float* ks = s_sc + (it % C::RING) * 2 * CH_KEYS + q2;
-                    const bool masked = pos_first - j * CH_KEYS < CH_KEYS - 1 || bad != 0;  // warp-uniform
-                    uint32_t sv[2][32];
-                    tmem_ld_16x256b_x8(s_addr, sv[0]);
-                    tmem_ld_16x256b_x8(s_addr + 64, sv[1]);
+                    const uint32_t bad = s_bad[it % C::RING] >> (4 * hh) & 15u;
+                    const float* ks = s_sc + (it % C::RING) * 2 * CH_KEYS + hh * CH_STEP + q2;
+                    const bool masked = pos_first - kb < CH_STEP - 1 || bad != 0;  // warp-uniform
+                    uint32_t sv[32];
+                    tmem_ld_16x256b_x8(sp, sv);
                     tmem_wait_ld();
-                    tmem_regs_ready(sv[0]);
-                    tmem_regs_ready(sv[1]);
+                    tmem_regs_ready(sv);
                     if constexpr (FP8) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < 8; ++i) {
                             const float2 f = *reinterpret_cast<const float2*>(ks + 8 * i);
-                            uint32_t* x = sv[i >> 3] + 4 * (i & 7);
+                            uint32_t* x = sv + 4 * i;
                             const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), f);
                             const float2 z = __fmul2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), f);
                             x[0] = __float_as_uint(y.x);
@@ -578,24 +554,23 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                         }
                     }
                     if (masked) {
-                        // keys 0 .. lim of the tile are seen
-                        const int pos0 = u.pos0 - j * CH_KEYS, ra = row0 + (lane >> 2);
+                        // keys 0 .. lim of the step are seen
+                        const int pos0 = u.pos0 - kb, ra = row0 + (lane >> 2);
                         const int lima = pos0 + (ra >> gs), limb = pos0 + ((ra + 8) >> gs);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            uint32_t* x = sv[i >> 3] + 4 * (i & 7);
+                        for (int i = 0; i < 8; ++i) {
                             const bool b = bad >> (i >> 1) & 1u;
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                if (b || 8 * i + q2 + e > lima) x[e] = 0xff800000u;  // -inf
-                                if (b || 8 * i + q2 + e > limb) x[2 + e] = 0xff800000u;
+                                if (b || 8 * i + q2 + e > lima) sv[4 * i + e] = 0xff800000u;  // -inf
+                                if (b || 8 * i + q2 + e > limb) sv[4 * i + 2 + e] = 0xff800000u;
                             }
                         }
                     }
                     float xa[2] = {-INFINITY, -INFINITY}, xb[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint32_t* x = sv[i >> 3] + 4 * (i & 7);
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t* x = sv + 4 * i;
                         xa[i & 1] = fmax3(xa[i & 1], __uint_as_float(x[0]), __uint_as_float(x[1]));
                         xb[i & 1] = fmax3(xb[i & 1], __uint_as_float(x[2]), __uint_as_float(x[3]));
                     }
@@ -608,68 +583,69 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     // row's maximum has grown by more than 2^8: the weights stay below 2^8
                     const bool mva = mxa > ma + kRescaleThreshold || ma == -INFINITY;
                     const bool mvb = mxb > mb + kRescaleThreshold || mb == -INFINITY;
-                    const float na = mva ? fmaxf(mxa, ma) : ma, nb = mvb ? fmaxf(mxb, mb) : mb;
-                    const bool rsa = mva && ma != -INFINITY, rsb = mvb && mb != -INFINITY;
-                    if (__any_sync(0xffffffffu, rsa || rsb)) {
-                        const float ala = rsa ? fast_exp2(ma - na) : 1.f, alb = rsb ? fast_exp2(mb - nb) : 1.f;
-                        la *= ala;
-                        lb *= alb;
-                        // (the scores of this tile were issued after the last P V had finished)
+                    if (__any_sync(0xffffffffu, mva || mvb)) {
+                        const float na = mva ? fmaxf(mxa, ma) : ma, nb = mvb ? fmaxf(mxb, mb) : mb;
+                        const bool rsa = mva && ma != -INFINITY, rsb = mvb && mb != -INFINITY;
+                        if (__any_sync(0xffffffffu, rsa || rsb)) {
+                            const float ala = rsa ? fast_exp2(ma - na) : 1.f, alb = rsb ? fast_exp2(mb - nb) : 1.f;
+                            la *= ala;
+                            lb *= alb;
+                            // O must be still: the P V of the step before has finished
+                            if (!ready(&pv_done[2 * t + ((cnt - 1) & 1)], ((cnt - 1) >> 1) & 1, s_abort)) continue;
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t ov[8];
-                            tmem_ld_16x256b_x2(o_base + t * D + c * 16, ov);
-                            tmem_wait_ld();
-                            tmem_regs_ready(ov);
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t ov[8];
+                                tmem_ld_16x256b_x2(o_base + t * D + c * 16, ov);
+                                tmem_wait_ld();
+                                tmem_regs_ready(ov);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * ((i & 2) ? alb : ala));
-                            tmem_st_16x256b_x2(o_base + t * D + c * 16, ov);
+                                for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * ((i & 2) ? alb : ala));
+                                tmem_st_16x256b_x2(o_base + t * D + c * 16, ov);
+                            }
                         }
+                        ma = na;
+                        mb = nb;
                     }
-                    ma = na;
-                    mb = nb;
                     // weights 2^(s sl2 - m), to TMEM as bf16 over the scores' first half.  bf16: a quarter of the
                     // exponentials on the FMA pipe (none / an eighth / a quarter / half of them there: 704 / 706 / 686 /
                     // 735 us for two 3.5K-token chunks; FP8 is bound by instructions: none)
                     const float2 sca = make_float2(sl2a, sl2a), scb = make_float2(sl2b, sl2b);
                     const float mua = ma == -INFINITY ? 0.f : -ma, mub = mb == -INFINITY ? 0.f : -mb;
                     float2 acca = make_float2(0.f, 0.f), accb = acca;
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t* x = sv[h] + 4 * i;
-                            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sca, make_float2(mua, mua));
-                            const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), scb, make_float2(mub, mub));
-                            float2 pa = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                            float2 pb = !FP8 && (i & 1) == 0 ? exp2_poly2(z) : make_float2(fast_exp2(z.x), fast_exp2(z.y));
-                            acca = __fadd2_rn(acca, pa);
-                            accb = __fadd2_rn(accb, pb);
-                            if constexpr (FP8) {
-                                const float2 f = *reinterpret_cast<const float2*>(ks + CH_KEYS + h * 64 + 8 * i);
-                                pa = __fmul2_rn(pa, f);
-                                pb = __fmul2_rn(pb, f);
-                            }
-                            pk[2 * i] = pack_bf16x2(pa.x, pa.y);
-                            pk[2 * i + 1] = pack_bf16x2(pb.x, pb.y);
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t* x = sv + 4 * i;
+                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sca, make_float2(mua, mua));
+                        const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), scb, make_float2(mub, mub));
+                        float2 pa = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                        float2 pb = !FP8 && (i & 1) == 0 ? exp2_poly2(z) : make_float2(fast_exp2(z.x), fast_exp2(z.y));
+                        acca = __fadd2_rn(acca, pa);
+                        accb = __fadd2_rn(accb, pb);
+                        if constexpr (FP8) {
+                            const float2 f = *reinterpret_cast<const float2*>(ks + CH_KEYS + 8 * i);
+                            pa = __fmul2_rn(pa, f);
+                            pb = __fmul2_rn(pb, f);
                         }
-                        tmem_st_16x128b_x8(s_addr + h * 32, pk);
+                        pk[2 * i] = pack_bf16x2(pa.x, pa.y);
+                        pk[2 * i + 1] = pack_bf16x2(pb.x, pb.y);
                     }
+                    tmem_st_16x128b_x8(sp, pk);
                     la += acca.x + acca.y;
                     lb += accb.x + accb.y;
                     tmem_wait_st();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[t]);
+                if (lane == 0) mbar_arrive(&p_full[2 * t + (cnt & 1)]);
             }
-            it0 += te - tb;
+            it0 += u.te - tb;
             la += __shfl_xor_sync(0xffffffffu, la, 1);
             lb += __shfl_xor_sync(0xffffffffu, lb, 1);
             la += __shfl_xor_sync(0xffffffffu, la, 2);
             lb += __shfl_xor_sync(0xffffffffu, lb, 2);
-            const bool ok = n_my == 0 || ready(&pv_done[t], (cnt - 1) & 1, s_abort);
+            const bool ok = n_my == 0 || ready(&pv_done[2 * t + ((cnt - 1) & 1)], ((cnt - 1) >> 1) & 1, s_abort);
             tc_fence_after();
             // ---- the piece's rows: finished, or a partial for the merge ----
             float va = 0.f, vb = 0.f;  // weights of the other buffer's sums; ua, ub of this one's (nothing seen: 0, as
@@ -857,7 +833,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
     } else {
         if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
-        // ===== warp 19: this CTA's pieces =====
+        // ===== warp 19: this CTA's pieces, and their Q: [128 / g tokens][g heads] boxes, one or two tiles =====
         if (lane == 0) {
             const long long N = plan.total();
             // every CTA's stretch holds two points at least, so that it owns a tile of each unit it lies in
@@ -874,6 +850,17 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 *reinterpret_cast<Piece*>(smem + C::OFF_PIECE + k * sizeof(Piece)) = pc;
                 mbar_arrive(&piece_full[k]);
                 ++np;
+                if (pc.rows == 0) return;
+                if (np > 1 && !(ok = !*s_abort && mbar_wait(q_empty, np & 1))) {  // the scores of the piece before are done
+                    *s_abort = 1;
+                    return;
+                }
+                mbar_arrive_expect_tx(q_full, pc.cost * C::TILE);
+                for (int t = 0; t < pc.cost; ++t)
+#pragma unroll
+                    for (int h = 0; h < C::HALVES; ++h)
+                        tma_load_3d(smem + C::OFF_Q + t * C::TILE + h * C::BOX, &tm_q, q_full, h * 64, pc.kvh * a.g,
+                                    pc.tok0 + t * (w / 2));
             };
             if (N > 0 && c < G) {
                 const long long lo = chunk_start(c, N, G), hi = chunk_start(c + 1, N, G);
@@ -887,7 +874,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     pc.pos0 = u.s.base() + u.rb * w;
                     pc.rows = u.rows;
                     pc.keys = u.keys;
-                    pc.tiles0 = u.tiles0;
+                    pc.keys0 = u.keys0;
                     pc.cost = u.cost;
                     pc.count = chunk_owner(u.U + static_cast<long long>(u.tiles - 1) * u.cost, N, G) - f + 1;
                     pc.first = f == c;
@@ -897,8 +884,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             }
             // the merge finds a split unit at the CTA of its first tile
             a.split_info[c] = split;
+            const int loaded = np;
             Piece none{};
             if (ok) put(none);
+            if (loaded > 0) mbar_wait(q_full, (loaded - 1) & 1);  // no copy in flight when the CTA leaves
         }
     }
     tc_fence_before();
