@@ -96,23 +96,6 @@ struct TCfg {
     static constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D, false, true);
 };
 
-// 2^x for two values on the FMA pipe (Cody-Waite split x = n + f, n = rint(x)); 0 below -125.
-// Degree-4 polynomial for 2^f on [-1/2, 1/2], minimax in relative error (2.7e-6 in fp32 Horner
-// form), produced by fit_exp2_poly.py's remez(4): the sums enter an fp32 output (lse), which the
-// degree-3 one's 7.5e-5 would show in.
-__device__ __forceinline__ float2 exp2_poly2(float2 x)
-{
-    const float2 t = __fadd2_rn(x, make_float2(kShifter, kShifter));
-    const float2 n = __fadd2_rn(t, make_float2(-kShifter, -kShifter));
-    const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
-    float2 p = __ffma2_rn(make_float2(0.009570102f, 0.009570102f), f, make_float2(0.05591786f, 0.05591786f));
-    p = __ffma2_rn(p, f, make_float2(0.24024744f, 0.24024744f));
-    p = __ffma2_rn(p, f, make_float2(0.6931218f, 0.6931218f));
-    p = __ffma2_rn(p, f, make_float2(0.9999993f, 0.9999993f));
-    return make_float2(x.x < -125.f ? 0.f : __uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                       x.y < -125.f ? 0.f : __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
-}
-
 // Four E4M3 codes -> fp16 pairs, exactly.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
 {
@@ -607,9 +590,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                         ma = na;
                         mb = nb;
                     }
-                    // weights 2^(s sl2 - m), to TMEM as bf16 over the scores' first half.  bf16: a quarter of the
-                    // exponentials on the FMA pipe (none / an eighth / a quarter / half of them there: 704 / 706 / 686 /
-                    // 735 us for two 3.5K-token chunks; FP8 is bound by instructions: none)
+                    // weights 2^(s sl2 - m), to TMEM as bf16 over the scores' first half.  Every exponential goes
+                    // through the hardware unit, where 2^-inf is exactly 0: none / an eighth / a quarter / half of them
+                    // as a polynomial on the FMA pipe took 592 / 601 / 607 / 647 us for two 3.5K-token chunks (and none
+                    // at all 602: they are hidden behind the products)
                     const float2 sca = make_float2(sl2a, sl2a), scb = make_float2(sl2b, sl2b);
                     const float mua = ma == -INFINITY ? 0.f : -ma, mub = mb == -INFINITY ? 0.f : -mb;
                     float2 acca = make_float2(0.f, 0.f), accb = acca;
@@ -620,7 +604,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                         const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sca, make_float2(mua, mua));
                         const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), scb, make_float2(mub, mub));
                         float2 pa = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                        float2 pb = !FP8 && (i & 1) == 0 ? exp2_poly2(z) : make_float2(fast_exp2(z.x), fast_exp2(z.y));
+                        float2 pb = make_float2(fast_exp2(z.x), fast_exp2(z.y));
                         acca = __fadd2_rn(acca, pa);
                         accb = __fadd2_rn(accb, pb);
                         if constexpr (FP8) {
