@@ -3,8 +3,10 @@
 // The query rows of (sequence b, KV head) are its tokens times the g heads of the
 // group, token-major, cut into blocks of 256 rows (w = 256 / g tokens).  A block
 // attends to the keys 0 .. (position of its last token), cut into tiles of 128: its
-// unit has that many tiles, each costing 1 where the block has at most 128 rows and 2
-// otherwise.  The costs of all units, in the order (sequence, head, block), form one
+// unit has that many tiles, each costing 3 where the block has at most 128 rows and 4
+// otherwise (the times that a tile takes then, about: 2600 and 3300 cycles; with 1 and 2 the
+// CTAs of a mixed batch's decoding sequences took twice as long as those of its chunks).
+// The costs of all units, in the order (sequence, head, block), form one
 // line of length N; CTA c of G takes the stretch [c N / G, (c + 1) N / G) of it: the
 // tiles whose first cost point lies there.  A unit that crosses a border is finished
 // by the merge from one partial per CTA.  Everything is computed on the device, in
@@ -17,6 +19,7 @@ namespace kvattn {
 
 constexpr int CH_ROWS = 256;  // query rows of a block
 constexpr int CH_KEYS = 128;  // keys of a tile
+constexpr int CH_COST1 = 3, CH_COST2 = 4;  // points of a tile with one and with two Q tiles
 
 // Sums in closed form, by shifts: one thread walks the plan at the head of every call.
 // Sum over i = 1 .. k of the tiles that base + i w keys fill, w = 1 << ws (4 .. 256).
@@ -47,11 +50,11 @@ struct ChunkSeq {
     __host__ __device__ long long cost(int k, int ws) const
     {
         const int full = take >> ws;
-        if (k <= full) return 2 * chunk_tiles_prefix(base(), ws, k);
+        if (k <= full) return CH_COST2 * chunk_tiles_prefix(base(), ws, k);
         const int rest = take - (full << ws);
         const int keys = base() + take;
         const long long tiles = keys > 0 ? (keys + CH_KEYS - 1) >> 7 : 0;
-        return 2 * chunk_tiles_prefix(base(), ws, full) + (2 * rest <= (1 << ws) ? 1 : 2) * tiles;
+        return CH_COST2 * chunk_tiles_prefix(base(), ws, full) + (2 * rest <= (1 << ws) ? CH_COST1 : CH_COST2) * tiles;
     }
     __host__ __device__ int blocks(int ws) const { return static_cast<int>((static_cast<long long>(take) + (1 << ws) - 1) >> ws); }
 };
@@ -74,7 +77,8 @@ struct ChunkUnit {
     int keys;        // keys that its last token sees
     int tiles;       // 128-key tiles of them
     int keys0;       // keys that the last token of the first 128 rows sees
-    int cost;        // points per tile
+    int qt;          // Q tiles of 128 rows: 1 or 2
+    __host__ __device__ int cost() const { return qt == 1 ? CH_COST1 : CH_COST2; }  // points per tile
 };
 
 // Where the batch lies in shared memory: raw offsets and lengths, and the line's prefix
@@ -99,9 +103,9 @@ struct ChunkPlan {
         u.rows = left * g;
         u.keys = max(u.s.base() + i0 + left, 0);
         u.tiles = (u.keys + CH_KEYS - 1) >> 7;
-        u.cost = u.rows <= CH_ROWS / 2 ? 1 : 2;
+        u.qt = u.rows <= CH_ROWS / 2 ? 1 : 2;
         // the first 128 rows end with token i0 + w / 2 - 1 (g <= 64: w / 2 >= 2); g = 1: w = 256
-        u.keys0 = u.cost == 1 ? u.keys : max(u.s.base() + i0 + w / 2, 0);
+        u.keys0 = u.qt == 1 ? u.keys : max(u.s.base() + i0 + w / 2, 0);
     }
 
     // the unit holding point x (0 <= x < total())
@@ -135,7 +139,7 @@ struct ChunkPlan {
     // the next unit with tiles; b = B behind the last one
     __host__ __device__ void next(ChunkUnit& u) const
     {
-        u.U += static_cast<long long>(u.cost) * u.tiles;
+        u.U += static_cast<long long>(u.cost()) * u.tiles;
         ++u.rb;
         while (u.b < B) {
             const int nb = u.s.blocks(ws);
@@ -155,9 +159,11 @@ struct ChunkPlan {
     // tiles [tb, te) of u whose first points lie in [lo, hi)
     __host__ __device__ bool piece(const ChunkUnit& u, long long lo, long long hi, int& tb, int& te) const
     {
-        const long long a = max(lo, u.U) - u.U, z = min(hi - u.U, static_cast<long long>(u.cost) * u.tiles);
-        tb = static_cast<int>((a + u.cost - 1) >> (u.cost - 1));
-        te = static_cast<int>((z + u.cost - 1) >> (u.cost - 1));
+        const uint32_t a = static_cast<uint32_t>(max(lo, u.U) - u.U);  // (a unit has less than 2^26 points)
+        const uint32_t z = static_cast<uint32_t>(min(hi - u.U, static_cast<long long>(u.cost()) * u.tiles));
+        auto tile = [&](uint32_t x) { return static_cast<int>(u.qt == 1 ? (x + CH_COST1 - 1) / CH_COST1 : (x + CH_COST2 - 1) / CH_COST2); };
+        tb = tile(a);
+        te = tile(z);
         return tb < te;
     }
 };

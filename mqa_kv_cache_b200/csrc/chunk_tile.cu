@@ -44,7 +44,7 @@ struct Piece {
     int rows, keys;
     int tb, te;  // tiles
     int keys0;   // keys that the first 128 rows see
-    int cost;    // 2: two Q tiles, 1: one
+    int qt;      // Q tiles of 128 rows: 1 or 2
     int count;   // pieces of the unit
     int first;   // whether this is the first of them
 };
@@ -58,7 +58,7 @@ __device__ __forceinline__ int piece_steps(const P& u, int t)
 {
     const int tiles = u.te - u.tb;
     auto upto = [&](int keys) { return max(min(2 * tiles, ((keys + CH_STEP - 1) >> 6) - 2 * u.tb), 0); };
-    if (u.cost == 2) return upto(t ? u.keys : u.keys0);
+    if (u.qt == 2) return upto(t ? u.keys : u.keys0);
     return (upto(u.keys) + 1 - t) >> 1;
 }
 
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         Piece u;
         for (int np = 0; ok && take(np, u); ++np) {
             ok = ready(FP8 ? q_ready : q_full, np & 1, s_abort);
-            const bool pair = u.cost == 2;
+            const bool pair = u.qt == 2;
             const int n0 = piece_steps(u, 0), n1 = piece_steps(u, 1), n = max(n0, n1);
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         uint32_t gn[2] = {0, 0};
         Piece u;
         for (int np = 0; ok && take(np, u); ++np) {
-            const bool pair = u.cost == 2;
+            const bool pair = u.qt == 2;
             const int n0 = piece_steps(u, 0), n1 = piece_steps(u, 1), n = max(n0, n1);
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             const volatile Piece& u = s_piece[n % PIECES];
             if (u.rows == 0) break;
             const int tb = u.tb;
-            const bool pair = u.cost == 2;  // two Q tiles; else one, its keys dealt out in steps
+            const bool pair = u.qt == 2;  // two Q tiles; else one, its keys dealt out in steps
             const int row0 = (pair ? t * 128 : 0) + r16;  // the warp's first row of the block
             const int pos_first = u.pos0 + (row0 >> gs);
             const bool active_warp = row0 < u.rows;
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 ok = ready(q_full, n & 1, s_abort);
                 if (!ok) break;
 #pragma unroll 2
-                for (int i = 0; i < u.cost * (D / 8); ++i) {
+                for (int i = 0; i < u.qt * (D / 8); ++i) {
                     const int id = i * 128 + tid, row = id / (D / 8), c8 = id % (D / 8);
                     uint4* q = reinterpret_cast<uint4*>(smem + C::OFF_Q + (row >> 7) * C::TILE + (c8 >> 3) * C::BOX + swz128(row & 127, c8 & 7));
                     const uint4 v = *q;
@@ -820,8 +820,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         // ===== warp 19: this CTA's pieces, and their Q: [128 / g tokens][g heads] boxes, one or two tiles =====
         if (lane == 0) {
             const long long N = plan.total();
-            // every CTA's stretch holds two points at least, so that it owns a tile of each unit it lies in
-            const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), N > 2 ? N >> 1 : 1));
+            // every CTA's stretch holds a tile's points at least, so that it owns a tile of each unit it lies in
+            const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), max(N / CH_COST2, 1ll)));
             int4 split = make_int4(0, 0, 0, 0);
             int np = 0;
             bool ok = true;
@@ -839,8 +839,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     *s_abort = 1;
                     return;
                 }
-                mbar_arrive_expect_tx(q_full, pc.cost * C::TILE);
-                for (int t = 0; t < pc.cost; ++t)
+                mbar_arrive_expect_tx(q_full, pc.qt * C::TILE);
+                for (int t = 0; t < pc.qt; ++t)
 #pragma unroll
                     for (int h = 0; h < C::HALVES; ++h)
                         tma_load_3d(smem + C::OFF_Q + t * C::TILE + h * C::BOX, &tm_q, q_full, h * 64, pc.kvh * a.g,
@@ -859,8 +859,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     pc.rows = u.rows;
                     pc.keys = u.keys;
                     pc.keys0 = u.keys0;
-                    pc.cost = u.cost;
-                    pc.count = chunk_owner(u.U + static_cast<long long>(u.tiles - 1) * u.cost, N, G) - f + 1;
+                    pc.qt = u.qt;
+                    pc.count = chunk_owner(u.U + static_cast<long long>(u.tiles - 1) * u.cost(), N, G) - f + 1;
                     pc.first = f == c;
                     if (pc.count > 1 && pc.first) split = make_int4(pc.tok0, pc.rows, pc.kvh, pc.count);
                     put(pc);
