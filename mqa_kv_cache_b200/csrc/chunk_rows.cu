@@ -77,8 +77,8 @@ struct RCfg {
     static constexpr int OFF_U = OFF_ML + RW * WR * 8;
     static constexpr int OFF_PIECE = OFF_U + (PAGED_MAX_B + 1) * 8;
     static constexpr int OFF_BAR = OFF_PIECE + (RPIECES * static_cast<int>(sizeof(RowPiece)) + 7) / 8 * 8;
-    // full[STAGES], empty[STAGES], q_full[2], q_empty[2], piece_full[RPIECES], piece_empty[RPIECES]
-    static constexpr int NBAR = 2 * STAGES + 4 + 2 * RPIECES;
+    // full[STAGES], empty[STAGES], q_full[2], q_empty[2], piece_full[RPIECES], piece_empty[RPIECES], met
+    static constexpr int NBAR = 2 * STAGES + 5 + 2 * RPIECES;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 64 + STAGES * 4 + 1024;
     static_assert(SMEM * CTAS <= 233472 - 1024 * CTAS, "shared memory");
@@ -132,23 +132,26 @@ __device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity, volatile i
 __device__ __forceinline__ uint32_t swz64(int r, int ch) { return static_cast<uint32_t>(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)); }
 
 // The partial slots of pieces i0 .. i1 - 1 (every `step`-th) of the unit whose first piece is CTA f's,
-// joined by `nthr` threads: into the unit's rows, or (unnormalised) into the slot of piece i0.
+// joined by `nthr` threads: into the unit's rows, or (unnormalised) into the slot of piece i0, with
+// (maximum, sum) beside it, as other threads still read the slot's own.  A group's partials are all
+// requested at once: a call waits for memory rows * D / 4 / nthr times.
 template <int D, int RM>
-__device__ void join_pieces(const ChunkArgs& a, int f, int i0, int i1, int step, const RowPiece& pc, bool last, int tid,
-                            int nthr)
+__device__ void join_pieces(const ChunkArgs& a, int gs, int f, int i0, int i1, int step, const RowPiece& pc, bool last,
+                            int tid, int nthr)
 {
-    constexpr int Q4 = D / 4, BATCH = 8;
-    const int rows = pc.n * a.g;
+    constexpr int Q4 = D / 4;
     auto slot = [f](int i) { return static_cast<long long>(i == 0 ? 2 * f + 1 : 2 * (f + i)) * RM; };
-    for (int idx = tid; idx < rows * Q4; idx += nthr) {
+    for (int idx = tid; idx < (pc.n << gs) * Q4; idx += nthr) {
         const int r = idx / Q4, q4 = idx - r * Q4;
         float M = -INFINITY, L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = i0; i < i1; i += BATCH * step) {
-            float2 ml[BATCH];
-            float4 o[BATCH];
+        for (int i = i0; i < i1; i += RGROUP * step) {
+            float2 ml[RGROUP];
+            float4 o[RGROUP];
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
+            for (int k = 0; k < RGROUP; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (i + k * step < i1) {
                     const long long s = slot(i + k * step) + r;
                     ml[k] = __ldcg(a.part_ml + s);
@@ -157,34 +160,29 @@ __device__ void join_pieces(const ChunkArgs& a, int f, int i0, int i1, int step,
             }
             float Mn = M;
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k)
-                if (i + k * step < i1) Mn = fmaxf(Mn, ml[k].x);
+            for (int k = 0; k < RGROUP; ++k) Mn = fmaxf(Mn, ml[k].x);
             const float mu = Mn == -INFINITY ? 0.f : Mn;
-            const float c = M == -INFINITY ? 0.f : fast_exp2(M - mu);
+            const float c = fast_exp2(M - mu);
             L *= c;
             acc = make_float4(acc.x * c, acc.y * c, acc.z * c, acc.w * c);
             M = Mn;
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                if (i + k * step < i1) {
-                    const float e = ml[k].x == -INFINITY ? 0.f : fast_exp2(ml[k].x - mu);
-                    L += e * ml[k].y;
-                    acc.x += e * o[k].x;
-                    acc.y += e * o[k].y;
-                    acc.z += e * o[k].z;
-                    acc.w += e * o[k].w;
-                }
+            for (int k = 0; k < RGROUP; ++k) {
+                const float e = fast_exp2(ml[k].x - mu);
+                L += e * ml[k].y;
+                acc.x += e * o[k].x;
+                acc.y += e * o[k].y;
+                acc.z += e * o[k].z;
+                acc.w += e * o[k].w;
             }
         }
         if (last) {
             const float inv = L > 0.f ? 1.f / L : 0.f;
-            const long long row = static_cast<long long>(pc.t0 + r / a.g) * a.H + static_cast<long long>(pc.kvh) * a.g + r % a.g;
+            const long long row = static_cast<long long>(pc.t0 + (r >> gs)) * a.H + (static_cast<long long>(pc.kvh) << gs) + (r & ((1 << gs) - 1));
             *reinterpret_cast<uint2*>(a.out + row * D + 4 * q4) =
                 make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
             if (q4 == 0 && a.lse) a.lse[row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
         } else {
-            // every thread of the row has read (m, l) before this one's place is rewritten: see the barrier
-            // at the caller, which lets all threads finish their reads first
             const long long s = slot(i0) + r;
             __stcg(reinterpret_cast<float4*>(a.part_o + s * D) + q4, acc);
             if (q4 == 0) __stcg(a.join_ml + s, make_float2(M, L));
@@ -210,6 +208,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
     uint64_t* q_empty = q_full + 2;
     uint64_t* piece_full = q_empty + 2;
     uint64_t* piece_empty = piece_full + RPIECES;
+    uint64_t* met = piece_empty + RPIECES;  // the consumer warps, at a barrier
     volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
     int* s_join = reinterpret_cast<int*>(smem + C::OFF_MISC) + 1;  // what this CTA is to join
     volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 64);  // [STAGES] 16-key groups without a page
@@ -229,6 +228,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
             mbar_init(&piece_full[i], 1);
             mbar_init(&piece_empty[i], RW + 1);
         }
+        mbar_init(met, RW);
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -422,7 +422,13 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
     const float sl2 = a.scale * kLog2e;
     int gs = 0;
     while ((1 << gs) < a.g) ++gs;
-    uint32_t it = 0;
+    uint32_t it = 0, meets = 0;
+    // barrier of the consumer warps: like every wait here, it gives up once a wait has run out
+    auto meet = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(met);
+        ready(met, meets++ & 1, s_abort);
+    };
     int n_split = 0;
     RowPiece pc, split[2];
     for (int np = 0; take_piece(np, pc); ++np) {
@@ -684,7 +690,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
                 l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
                 if (r0 == 0) s_ml[warp * WR + n * 8 + 2 * cq + e] = make_float2(m[n][e], l[n][e]);
             }
-        named_bar_sync(1, RW * 32);
+        meet();
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -716,7 +722,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
 #pragma unroll
                     for (int e = 0; e < 4; ++e) so[(n * 8 + (e & 1)) * C::SCR + i * 16 + (e >> 1) * CS] = o[n][i][e];
         }
-        named_bar_sync(1, RW * 32);
+        meet();
         if (sub < 2) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
@@ -731,7 +737,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
 #pragma unroll
                 for (int e = 0; e < 2; ++e) s_ml[warp * WR + n * 8 + 2 * cq + e] = make_float2(m[n][e], l[n][e]);
         }
-        named_bar_sync(1, RW * 32);
+        meet();
         // ---- the rows: finished, or a partial ----
         const long long slot = static_cast<long long>(2 * c + (c == pc.first ? 1 : 0)) * RM;
         for (int idx = threadIdx.x; idx < rows * (D / 4); idx += RW * 32) {
@@ -751,7 +757,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
                 if (q4 == 0) __stcg(a.part_ml + slot + r, ml);
             }
         }
-        named_bar_sync(1, RW * 32);
+        meet();
         if (pc.count > 1) split[n_split++ & 1] = pc;  // at most the first and the last unit of the stretch
     }
 
@@ -776,16 +782,16 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
             }
             *s_join = go;
         }
-        named_bar_sync(1, RW * 32);
+        meet();
         bool go = *s_join;
-        named_bar_sync(1, RW * 32);
+        meet();
         if (!go) continue;
-        join_pieces<D, RM>(a, s.first, i0, i1, 1, s, groups == 1, threadIdx.x, RW * 32);
+        join_pieces<D, RM>(a, gs, s.first, i0, i1, 1, s, groups == 1, threadIdx.x, RW * 32);
         if (groups == 1) continue;
-        named_bar_sync(1, RW * 32);  // everyone has read the group's (m, l)
+        meet();  // everyone has read the group's (m, l)
         const long long lead = static_cast<long long>(i0 == 0 ? 2 * s.first + 1 : 2 * (s.first + i0)) * RM;
         for (int r = threadIdx.x; r < s.n * a.g; r += RW * 32) __stcg(a.part_ml + lead + r, __ldcg(a.join_ml + lead + r));
-        named_bar_sync(1, RW * 32);
+        meet();
         if (threadIdx.x == 0) {
             __threadfence();
             go = atomicAdd(ucnt, 1) == groups - 1;
@@ -795,10 +801,10 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
             }
             *s_join = go;
         }
-        named_bar_sync(1, RW * 32);
+        meet();
         go = *s_join;
-        named_bar_sync(1, RW * 32);
-        if (go) join_pieces<D, RM>(a, s.first, 0, s.count, RGROUP, s, true, threadIdx.x, RW * 32);
+        meet();
+        if (go) join_pieces<D, RM>(a, gs, s.first, 0, s.count, RGROUP, s, true, threadIdx.x, RW * 32);
     }
 }
 
