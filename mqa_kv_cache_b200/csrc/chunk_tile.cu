@@ -517,8 +517,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 }
                 if (FP8 && k == 0) {  // (the scores wait for the converted Q rows)
                     const float* qs = s_qs + (n & 1) * CH_ROWS + row0 + (lane >> 2);
-                    sl2a = sl2 * qs[0];
-                    sl2b = sl2 * qs[8];
+                    // not 0, as that times the -inf of a key out of sight is no number (a tiny or zero row: its
+                    // scores are 0 either way)
+                    sl2a = fmaxf(sl2 * qs[0], 0x1p-126f);
+                    sl2b = fmaxf(sl2 * qs[8], 0x1p-126f);
                 }
                 if (active_warp) {
                     const uint32_t bad = s_bad[it % C::RING] >> (4 * hh) & 15u;

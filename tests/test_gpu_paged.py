@@ -148,6 +148,39 @@ def test_append_leaves_out_what_has_no_place(K):
     assert run([0, 2], [18], [[0, 1]]) == (0, 2)                         # tokens 2, 3 belong to nobody
 
 
+def _rule(x):
+    """Codes and scales by the rule in fp32 on the CPU (IEEE divisions)."""
+    s = x.float().abs().amax(-1) / 448.0
+    c = (x.float() / torch.where(s > 0, s, 1.0)[..., None]).to(F8)
+    return c, s
+
+
+@pytest.mark.parametrize("T", [1, 700])
+def test_append_fp8_codes_are_the_divided_quotients(K, T):
+    """bf16 values and their row's maximum are small integers times powers of two, so quotients on or next to a
+    border between codes are frequent; rows of every size that bf16 has, and rows whose scale's reciprocal is no
+    normal number: every code and scale of V is the rule's."""
+    heads, d, page = 4, 128, 64
+    g = W.generator(77)
+    v = torch.randn(T, heads, d, generator=g).bfloat16()
+    small = (torch.randint(-128, 129, (T, heads, d), generator=g).float() * 2.0 ** torch.randint(-9, 1, (T, heads, d), generator=g)).bfloat16()
+    v[:, 1] = small[:, 1]
+    for i, e in enumerate((-133, -126, -118, -100, -92, -40, 40, 100, 109, 120)):  # powers of two of whole rows
+        v[i % T, 2] = (small[i % T, 2].float() * 2.0 ** -7 * 2.0 ** max(e, -126) * (2.0 ** (e + 126) if e < -126 else 1.0)).bfloat16()
+    v[0, 3] = 0
+    lens = [T]
+    cu, ln, table, n_pages = R.batch(lens, [0], page, 78)
+    cos, sin = torch.ones(T, d // 2, device="cuda"), torch.zeros(T, d // 2, device="cuda")  # no rotation: K by the rule too
+    kc, vc = (torch.zeros(n_pages, heads, page, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(n_pages, heads, page, device="cuda") for _ in range(2))
+    K.kv_append_paged_rope_fp8(v.cuda(), v.cuda(), *_cuda(cu, ln, table), kc, ks, vc, vs, cos, sin)
+    c, s = _rule(v)
+    pg, row = R.places(cu, ln, table, page, 0)
+    for codes, scales in ((kc, ks), (vc, vs)):
+        assert torch.equal(scales.cpu()[pg, :, row], s)
+        assert torch.equal(codes.cpu()[pg, :, row].view(F8).float(), c.float())
+
+
 # ---- read back ----------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("lens,heads,d,page", [([1], 1, 64, 16), ([0, 17, 64, 130], 2, 128, 16), ([300, 5], 8, 64, 128),
@@ -286,6 +319,41 @@ def test_fp8_rows_of_very_different_size(K, n):
     assert _case(K, [n], [500], 4, 1, 128, 16, True, spread=4.0, seed=10, max_q=n) == 0
 
 
+@pytest.mark.parametrize("n,H,Hk,d", [(1, 8, 2, 128), (3, 8, 1, 64), (1, 32, 2, 128), (50, 4, 1, 128), (300, 2, 1, 64)])
+def test_every_fp8_code(K, n, H, Hk, d):
+    """Pages that hold all finite codes, subnormal ones and both zeros among them, under scales of 2^-12 .. 2^12."""
+    page, ctx = 32, 400
+    cu, lens, table, n_pages = R.batch([n], [ctx], page, 210)
+    g = W.generator(211)
+    finite = torch.tensor([c for c in range(256) if c & 0x7F != 0x7F], dtype=torch.uint8)
+    tensors, deq = [], []
+    for _ in range(2):
+        codes = finite[torch.randint(0, len(finite), (n_pages, Hk, page, d), generator=g)]
+        codes[:, :, ::3] &= 0x8F  # rows of subnormal codes and the smallest normal ones
+        sc = 2.0 ** torch.randint(-12, 1, (n_pages, Hk, page), generator=g).float() * (1 + torch.rand(n_pages, Hk, page, generator=g)) / 448
+        tensors += [codes.cuda(), sc.cuda()]
+        deq.append(codes.view(F8).double() * sc.double()[..., None])
+    q, st = _q(n, H, d, 212), _status()
+    out, lse = K.attn_chunk_paged_fp8(q.cuda(), *_cuda(cu, lens, table), *tensors, 0.5, max_q=n, dev_status=st)
+    assert int(st) == 0
+    R.check(out, lse, R.attention(q, cu, lens, table, page, *deq, 0.5, fp16_weights=True), "all codes")
+
+
+@pytest.mark.parametrize("e", [-60, 0, 60])
+@pytest.mark.parametrize("n", [1, 40])
+def test_fp8_queries_of_any_size(K, n, e):
+    """Query rows around 2^e, elements of a row up to 2^12 apart, one row zero: FP8 attention takes them through fp16."""
+    page, d, H, Hk, ctx = 16, 128, 4, 2, 200
+    cu, lens, table, n_pages = R.batch([n], [ctx], page, 220)
+    tensors, kd, vd = _cache(n_pages, Hk, page, d, True, 221)
+    g = W.generator(222)
+    q = (torch.randn(n, H, d, generator=g) * 2.0 ** torch.randint(-12, 1, (n, H, d), generator=g) * 2.0 ** e).bfloat16()
+    q[0, 1] = 0
+    scale = 2.0 ** -e
+    out, lse = K.attn_chunk_paged_fp8(q.cuda(), *_cuda(cu, lens, table), *tensors, scale, max_q=n)
+    R.check(out, lse, R.attention(q, cu, lens, table, page, kd, vd, scale, fp16_weights=True), f"2^{e}")
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_without_a_bound_on_the_chunks(K, fp8):
     assert _case(K, [1, 1, 1], [100, 30, 0], 8, 2, 128, 16, fp8, max_q=None) == 0
@@ -347,6 +415,14 @@ def test_long_cache_few_heads(K):
     for fp8 in (False, True):
         for n in (1, 3):
             assert _case(K, [n], [20000 - n], 8, 1, 128, 64, fp8, seed=41, max_q=n, poison=False) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("ns,ctx,H,Hk,d", [([40], [19960], 4, 1, 128), ([1, 33, 1], [9000, 6000, 5], 8, 1, 64),
+                                           ([260], [9000], 1, 1, 128), ([9], [20000], 64, 1, 128)])
+def test_blocks_shared_by_many_ctas(K, ns, ctx, H, Hk, d, fp8):
+    """Few blocks of query rows over long caches: one block's keys are spread over most of the card."""
+    assert _case(K, ns, ctx, H, Hk, d, 64, fp8, seed=45, max_q=max(ns), poison=False) == 0
 
 
 def test_many_sequences(K):
@@ -428,6 +504,19 @@ def test_one_workspace_for_calls_of_other_shapes(K, fp8, n):
         q = _q(int(cu[-1]), H, 128, 73)
         out, lse = _chunk(K, fp8, q.cuda(), *_cuda(cu, lens, table), *tensors, 0.09, max_q=n, ws=ws)
         R.check(out, lse, R.attention(q, cu, lens, table, 32, kd, vd, 0.09, fp16_weights=fp8), f"{ns} {ctx}")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_one_workspace_for_both_kinds_of_call(K, fp8):
+    """Single tokens, chunks, then single tokens again on one workspace; its counters are zero after each."""
+    ws = K.workspace(max(K.attn_chunk_paged_workspace_bytes(3, 400, m, 8, 1, 128) for m in (1, 4, 130)))
+    for turn, (ns, ctx) in enumerate((([1, 1], [9000, 30]), ([130, 1], [900, 3000]), ([4, 1, 2], [5000, 0, 77]), ([1], [12000]))):
+        cu, lens, table, n_pages = R.batch(ns, ctx, 64, 75)
+        tensors, kd, vd = _cache(n_pages, 1, 64, 128, fp8, 76)
+        q = _q(int(cu[-1]), 8, 128, 77)
+        out, lse = _chunk(K, fp8, q.cuda(), *_cuda(cu, lens, table), *tensors, 0.09, max_q=max(ns), ws=ws)
+        R.check(out, lse, R.attention(q, cu, lens, table, 64, kd, vd, 0.09, fp16_weights=fp8), f"turn {turn}")
+        assert not ws[:65536].any()
 
 
 def test_small_workspaces_and_foreign_tensors_are_refused(K):
