@@ -216,16 +216,19 @@ __global__ void __launch_bounds__(AP_THREADS) paged_append_kernel(PagedAppendArg
 }
 
 // ---- FP8 pages -> contiguous bf16 rows ----------------------------------------------
-// bf16(code * scale), one rounding.  D / 16 lanes per row, sixteen codes (one 16-byte
-// load, two 16-byte stores) each; a block takes RD_ROWS consecutive rows of one (batch,
-// KV head), K and V, so that their loads are all in flight together.
+// bf16(code * scale), one rounding.  D / 8 lanes per row, eight codes (an 8-byte load, a
+// 16-byte store) each, so that a warp's stores are whole runs of 512 bytes; a thread takes
+// RD_ROWS rows of K and V, all requested before the first is written.  Both streams pass
+// once: they are marked so.  163,508 rows (8 x 128), 1.02 GB: 171 us as timed here (sixteen
+// codes a lane, one row: 200; one row of eight: 190; two rows without the marks: 172).
 constexpr int RD_THREADS = 256;
+constexpr int RD_ROWS = 2;
 
 template <int D>
 __global__ void __launch_bounds__(RD_THREADS) paged_read_kernel(PagedReadArgs a)
 {
-    constexpr int LPR = D / 16;
-    constexpr int RPB = RD_THREADS / LPR;  // rows per block
+    constexpr int LPR = D / 8;
+    constexpr int RPB = RD_THREADS / LPR;  // rows per pass of a block
     pdl_wait();
     pdl_trigger();
     const PagedBatch& p = a.p;
@@ -233,33 +236,41 @@ __global__ void __launch_bounds__(RD_THREADS) paged_read_kernel(PagedReadArgs a)
     const int raw = p.seq_lens[b];
     const int len = min(max(raw, 0), min(a.T_max, p.max_pages << p.page_shift));
     if (raw != len && blockIdx.x == 0 && threadIdx.x == 0) report_status(p.dev_status, KVATTN_STATUS_BAD_LENGTH);
-    const int r = blockIdx.x * RPB + threadIdx.x / LPR, ln = threadIdx.x % LPR;
-    if (r >= len) return;
-    const int page = p.page_table[static_cast<long long>(b) * p.max_pages + (r >> p.page_shift)];
-    if (page < 0 || page >= p.n_pages) {
-        if (ln == 0) report_status(p.dev_status, KVATTN_STATUS_BAD_INDEX);
-        return;
-    }
-    const long long src = ((static_cast<long long>(page) * a.Hk + h) << p.page_shift) + (r & ((1 << p.page_shift) - 1));
-    const uint4 kc = __ldg(reinterpret_cast<const uint4*>(a.k_codes + src * D) + ln);
-    const uint4 vc = __ldg(reinterpret_cast<const uint4*>(a.v_codes + src * D) + ln);
-    const float ks = __ldg(a.k_scales + src), vs = __ldg(a.v_scales + src);
-    const long long dst = (static_cast<long long>(blockIdx.y) * a.T_max + r) * D + ln * 16;
-    auto put = [&](kvattn_bf16* out, uint4 c, float s) {
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        uint32_t o[8];
+    const int r0 = blockIdx.x * (RPB * RD_ROWS) + threadIdx.x / LPR, ln = threadIdx.x % LPR;
+    uint2 kc[RD_ROWS], vc[RD_ROWS];
+    float ks[RD_ROWS], vs[RD_ROWS];
+    bool have[RD_ROWS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 x = e4m3x2_to_f32(static_cast<uint16_t>(w[i])), y = e4m3x2_to_f32(static_cast<uint16_t>(w[i] >> 16));
-            o[2 * i] = pack_bf16x2(x.x * s, x.y * s);
-            o[2 * i + 1] = pack_bf16x2(y.x * s, y.y * s);
+    for (int i = 0; i < RD_ROWS; ++i) {
+        const int r = r0 + i * RPB;
+        have[i] = r < len;
+        if (!have[i]) continue;
+        const int page = p.page_table[static_cast<long long>(b) * p.max_pages + (r >> p.page_shift)];
+        if (page < 0 || page >= p.n_pages) {
+            if (ln == 0) report_status(p.dev_status, KVATTN_STATUS_BAD_INDEX);
+            have[i] = false;
+            continue;
         }
-        uint4* d = reinterpret_cast<uint4*>(out + dst);
-        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    };
-    put(a.k_out, kc, ks);
-    put(a.v_out, vc, vs);
+        const long long src = ((static_cast<long long>(page) * a.Hk + h) << p.page_shift) + (r & ((1 << p.page_shift) - 1));
+        kc[i] = __ldcs(reinterpret_cast<const uint2*>(a.k_codes + src * D) + ln);
+        vc[i] = __ldcs(reinterpret_cast<const uint2*>(a.v_codes + src * D) + ln);
+        ks[i] = __ldg(a.k_scales + src);
+        vs[i] = __ldg(a.v_scales + src);
+    }
+#pragma unroll
+    for (int i = 0; i < RD_ROWS; ++i) {
+        if (!have[i]) continue;
+        const long long dst = (static_cast<long long>(blockIdx.y) * a.T_max + r0 + i * RPB) * D + ln * 8;
+        auto put = [&](kvattn_bf16* out, uint2 c, float s) {
+            auto two = [s](uint32_t codes) {
+                const float2 x = e4m3x2_to_f32(static_cast<uint16_t>(codes));
+                return pack_bf16x2(x.x * s, x.y * s);
+            };
+            __stcs(reinterpret_cast<uint4*>(out + dst), make_uint4(two(c.x), two(c.x >> 16), two(c.y), two(c.y >> 16)));
+        };
+        put(a.k_out, kc[i], ks[i]);
+        put(a.v_out, vc[i], vs[i]);
+    }
 }
 
 }  // namespace
@@ -285,7 +296,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, bool fp8, int num_sms,
 
 cudaError_t launch_paged_read(const PagedReadArgs& a, cudaStream_t stream)
 {
-    const int rows = RD_THREADS / (a.d / 16);
+    const int rows = RD_THREADS / (a.d / 8) * RD_ROWS;
     const int cap = a.p.max_pages << a.p.page_shift;
     const int most = a.T_max < cap ? a.T_max : cap;  // no row beyond both is read
     const dim3 grid((most + rows - 1) / rows, a.p.B * a.Hk);
