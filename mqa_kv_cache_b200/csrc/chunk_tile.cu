@@ -24,6 +24,8 @@
 // their scores and the P V product takes them from there.  (128 keys at a time, where the
 // next scores wait for the P V that reads the weights in their place, the chain scores -
 // softmax - P V took 3960 cycles a tile against 2050 of the products alone.)
+#include <type_traits>
+
 #include "chunk_plan.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -300,8 +302,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
     };
 
     if (warp == 17) {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
         // ===== K/V pages: lane i takes box i of a tile (page, and for bf16 its 64-column half) =====
         const int bp_shift = min(p.page_shift, 7);  // rows of a box: a page's, 128 at most
         const int bp = 1 << bp_shift;
@@ -378,8 +379,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             for (uint32_t i = x > R ? x - R : 0; i < x; ++i) mbar_wait(&full[i % R], (i / R) & 1);
         }
     } else if (warp == 16) {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
         // ===== scores: S_t = Q K^T, a step ahead of the softmax (while that works on step i, step i + 1 is
         // multiplied), into half g % 2 of buffer t for its step number g =====
         const uint32_t el = elect_one();
@@ -426,8 +426,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         mbar_wait(done, 0);
         __syncwarp();
     } else if (warp == 18) {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
         // ===== O_t += P V, step by step =====
         const uint32_t el = elect_one();
         const uint32_t skv = smem_u32(smem + C::OFF_KV);
@@ -465,8 +464,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         mbar_wait(done, 0);
         __syncwarp();
     } else if (warp < 16) {
-        // registers: 640 threads at 96 = 512 x 104 + 128 x 64; with FP8 768 at 80 = 512 x 96 + 128 x 40 + 128 x 56
-        if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;" ::: "memory");
+        // registers: 640 threads at 96 = 512 x 104 + 128 x 64; with FP8 768 at 80 = 512 x 88 + 128 x 64 + 128 x 64
+        if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;" ::: "memory");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
         // ===== softmax + epilogue: warps 0-7 buffer 0, warps 8-15 buffer 1, 16 rows each =====
         // A row's scores are spread over a lane quad: thread (g, q) = (lane / 4, lane % 4) holds, of rows g and
@@ -730,7 +729,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         }
     } else if (warp >= 20) {
         if constexpr (FP8) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
             // ===== Q -> fp16 in place; codes -> 16-bit tiles in the 128-byte-swizzled layout: K fp16, V bf16 =====
             // K's products need no range beyond Q's and the codes', and fp16 is one conversion for two codes; the
             // weights, times the values' scales, need bf16's.
@@ -822,8 +821,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             }
         }
     } else {
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
         // ===== warp 19: this CTA's pieces, and their Q: [128 / g tokens][g heads] boxes, one or two tiles =====
         if (lane == 0) {
             const long long N = plan.total();
@@ -892,57 +890,63 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
 // ---- merge of the split units ------------------------------------------------------
 // One warp per query row: with M = max m_i over the partials and w_i = 2^(m_i - M),
 // out = sum w_i O_i / sum w_i l_i and lse = ln 2 (M + log2 sum w_i l_i), in the
-// partials' order.
+// partials' order.  Lane i holds (m, l) of partial i, 32 at a time, and eight partials'
+// rows are in flight together, so a row waits for memory 2 + count / 8 times.  As many warps
+// as the call's blocks can have rows; most units are whole, and their warps only look.
 constexpr int TM_WARPS = 8;
-constexpr int TM_BLOCKS = 16;  // per unit: 32 rows a pass.  (4 blocks: splits over many CTAs took twice as long.)
 
 template <int D>
 __global__ void __launch_bounds__(TM_WARPS * 32) chunk_tile_merge_kernel(ChunkArgs a)
 {
-    constexpr int PL = D / 32;
+    constexpr int PL = D / 32, BATCH = 8;
+    using Vec = typename std::conditional<PL == 4, float4, float2>::type;
     pdl_wait();
     pdl_trigger();
     const int f = blockIdx.x;
     const int4 info = a.split_info[f];
-    const int lane = threadIdx.x & 31;
-    const int count = info.w;
-    if (count < 2) return;
-    for (int row = blockIdx.y * TM_WARPS + (threadIdx.x >> 5); row < info.y; row += TM_WARPS * TM_BLOCKS) {
-        float M = -INFINITY;
-        for (int i = lane; i < count; i += 32)
-            M = fmaxf(M, a.part_ml[static_cast<long long>(i == 0 ? 2 * f + 1 : 2 * (f + i)) * CH_ROWS + row].x);
+    const int lane = threadIdx.x & 31, row = blockIdx.y * TM_WARPS + (threadIdx.x >> 5), count = info.w;
+    if (count < 2 || row >= info.y) return;
+    auto slot = [&](int i) { return static_cast<long long>(i == 0 ? 2 * f + 1 : 2 * (f + i)) * CH_ROWS + row; };
+    float M = -INFINITY, L = 0.f, acc[PL];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float mu = M == -INFINITY ? 0.f : M;
-        float L = 0.f, acc[PL];
+    for (int k = 0; k < PL; ++k) acc[k] = 0.f;
+    for (int i0 = 0; i0 < count; i0 += 32) {
+        const int n = min(32, count - i0);
+        const float2 ml = lane < n ? __ldcg(a.part_ml + slot(i0 + lane)) : make_float2(-INFINITY, 0.f);
+        float Mn = fmaxf(M, ml.x);
 #pragma unroll
-        for (int i = 0; i < PL; ++i) acc[i] = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < count; ++i) {
-            const long long pr = static_cast<long long>(i == 0 ? 2 * f + 1 : 2 * (f + i)) * CH_ROWS + row;
-            const float2 ml = a.part_ml[pr];
-            const float wi = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mu);
-            L += wi * ml.y;
-            const float* o = a.part_o + pr * D + lane * PL;
-            if constexpr (PL == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(o);
-                acc[0] += wi * v.x;
-                acc[1] += wi * v.y;
-                acc[PL - 2] += wi * v.z;
-                acc[PL - 1] += wi * v.w;
-            } else {
-                const float2 v = *reinterpret_cast<const float2*>(o);
-                acc[0] += wi * v.x;
-                acc[1] += wi * v.y;
+        for (int o = 16; o > 0; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, o));
+        const float mu = Mn == -INFINITY ? 0.f : Mn, c = fast_exp2(M - mu);
+        M = Mn;
+        const float wl = fast_exp2(ml.x - mu);
+        float sum = wl * ml.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        L = L * c + sum;
+#pragma unroll
+        for (int k = 0; k < PL; ++k) acc[k] *= c;
+        for (int i = 0; i < n; i += BATCH) {
+            Vec v[BATCH];
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j)
+                if (i + j < n) v[j] = __ldcg(reinterpret_cast<const Vec*>(a.part_o + slot(i0 + i + j) * D) + lane);
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const float w = __shfl_sync(0xffffffffu, wl, (i + j) & 31);
+                if (i + j < n) {
+                    const float* x = reinterpret_cast<const float*>(&v[j]);
+#pragma unroll
+                    for (int k = 0; k < PL; ++k) acc[k] += w * x[k];
+                }
             }
         }
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        const long long orow = (static_cast<long long>(info.x) + row / a.g) * a.H + static_cast<long long>(info.z) * a.g + row % a.g;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * PL);
-#pragma unroll
-        for (int i = 0; i < PL; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-        if (lane == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
     }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const long long orow = (static_cast<long long>(info.x) + row / a.g) * a.H + static_cast<long long>(info.z) * a.g + row % a.g;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * PL);
+#pragma unroll
+    for (int k = 0; k < PL; k += 2) dst[k / 2] = pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
 }
 
 template <int D, bool FP8>
@@ -962,7 +966,8 @@ cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& tm_q, const CUte
     e = launch_pdl(chunk_tile_kernel<D, FP8>, dim3(grid), dim3(TCfg<D, FP8>::THREADS), TCfg<D, FP8>::SMEM, stream, tm_q,
                    tm_k, tm_v, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(chunk_tile_merge_kernel<D>, dim3(grid, TM_BLOCKS), dim3(TM_WARPS * 32), 0, stream, a);
+    const int rows = a.max_q < CH_ROWS / a.g ? a.max_q * a.g : CH_ROWS;
+    return launch_pdl(chunk_tile_merge_kernel<D>, dim3(grid, (rows + TM_WARPS - 1) / TM_WARPS), dim3(TM_WARPS * 32), 0, stream, a);
 }
 
 }  // namespace
