@@ -16,7 +16,7 @@
 // Warps: 0-7 / 8-15 softmax of the two buffers (16 rows a warp, 64 scores a thread: half the
 // time of a thread per row, which the chain scores - softmax - P V - next scores waits for),
 // 16 issues the scores' MMAs, 18 the values', 17 loads K/V pages (one box per page and
-// 64-column half, page entries fetched one tile ahead), 19 hands out the pieces and loads Q.  FP8: warps 20-23 turn the
+// 64-column half, page entries fetched one tile ahead), 19 hands out the pieces and loads Q.  FP8: warps 20-27 turn the
 // codes of each landed tile into bf16 (exact) in the layout that the MMAs read; the keys'
 // scales multiply the scores and the values' scales the weights, in fp32.
 // TMEM: S0 | S1 | O0 | O1.  Scores are computed 64 keys at a time in either half of their 128
@@ -73,7 +73,11 @@ struct TCfg {
     static constexpr int NS = (FP8 ? 3 : 4) * 2 / HALVES;  // bf16 K/V slots
     static constexpr int LS = FP8 ? 4 / HALVES : 0;        // code slots
     static constexpr int RING = 8;                     // tiles whose page flags (and scales) are kept
-    static constexpr int THREADS = FP8 ? 768 : 640;
+    // Warps that widen codes.  8 (40 registers each) against 4 (64): 16 x 8 tokens over 8K rows 113 / 131 us, four
+    // 2K prompts 278 / 303, 2 x 40 tokens 20 / 23.5, but 1021 tokens over 31K rows on one KV head 1164 / 1090 (there
+    // they wait for the softmax, and take its issue slots).
+    static constexpr int CW = FP8 ? 8 : 0;
+    static constexpr int THREADS = 640 + 32 * CW;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_LAND = OFF_KV + NS * TILE;
@@ -88,8 +92,8 @@ struct TCfg {
     // kv_full[NS], kv_empty[NS], land_full[LS], land_empty[LS], q_full, q_empty, s_full[4], p_full[4], pv_done[4],
     // joined[2], piece_full[PIECES], piece_empty[PIECES], done, q_ready
     static constexpr int NBAR = 2 * NS + 2 * LS + 18 + 2 * PIECES;
-    // warps that take every piece: 16 of the softmax, both MMA warps, K/V loads, 4 of the widening
-    static constexpr int TAKERS = FP8 ? 23 : 19;
+    // warps that take every piece: 16 of the softmax, both MMA warps, K/V loads, those of the widening
+    static constexpr int TAKERS = 19 + CW;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + RING * 4 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
@@ -230,12 +234,12 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&kv_full[i], FP8 ? 4 : 1);
+            mbar_init(&kv_full[i], FP8 ? C::CW : 1);
             mbar_init(&kv_empty[i], 1);
         }
         for (int i = 0; i < LS; ++i) {
             mbar_init(&land_full[i], 1);
-            mbar_init(&land_empty[i], 4);
+            mbar_init(&land_empty[i], C::CW);
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             mbar_init(&piece_empty[i], C::TAKERS);
         }
         mbar_init(done, 2);
-        mbar_init(q_ready, 4);
+        mbar_init(q_ready, FP8 ? C::CW : 1);
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         mbar_wait(done, 0);
         __syncwarp();
     } else if (warp < 16) {
-        // registers: 640 threads at 96 = 512 x 104 + 128 x 64; with FP8 768 at 80 = 512 x 88 + 128 x 64 + 128 x 64
+        // registers: 640 threads at 96 = 512 x 104 + 128 x 64; with FP8 896 at 72 >= 512 x 88 + 128 x 64 + 256 x 40
         if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;" ::: "memory");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
         // ===== softmax + epilogue: warps 0-7 buffer 0, warps 8-15 buffer 1, 16 rows each =====
@@ -729,7 +733,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         }
     } else if (warp >= 20) {
         if constexpr (FP8) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
             // ===== Q -> fp16 in place; codes -> 16-bit tiles in the 128-byte-swizzled layout: K fp16, V bf16 =====
             // K's products need no range beyond Q's and the codes', and fp16 is one conversion for two codes; the
             // weights, times the values' scales, need bf16's.
@@ -747,8 +751,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 ok = ready(q_full, n & 1, s_abort);
                 if (!ok) break;
 #pragma unroll 2
-                for (int i = 0; i < u.qt * (D / 8); ++i) {
-                    const int id = i * 128 + tid, row = id / (D / 8), c8 = id % (D / 8);
+                for (int i = 0; i < u.qt * (D / 8) * 4 / C::CW; ++i) {
+                    const int id = i * (32 * C::CW) + tid, row = id / (D / 8), c8 = id % (D / 8);
                     uint4* q = reinterpret_cast<uint4*>(smem + C::OFF_Q + (row >> 7) * C::TILE + (c8 >> 3) * C::BOX + swz128(row & 127, c8 & 7));
                     const uint4 v = *q;
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -783,16 +787,16 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                         if (!ok) break;
                         const uint32_t bad = s_bad[it % C::RING];
                         const bool partial = nv < CH_KEYS || bad != 0;
-                        if (kv == 0 && partial && (tid >= nv || (bad >> (tid / 16) & 1u))) {
+                        if (kv == 0 && partial && tid < CH_KEYS && (tid >= nv || (bad >> (tid / 16) & 1u))) {
                             float* sc = s_sc + (it % C::RING) * 2 * CH_KEYS + tid;
                             sc[0] = 0.f;
                             sc[CH_KEYS] = 0.f;
                         }
                         const uint8_t* src = smem + C::OFF_LAND + ls * C::CODES;
                         uint8_t* dst = smem + C::OFF_KV + slot * C::TILE + (ch >> 2) * C::BOX;
-#pragma unroll 2
-                        for (int i = 0; i < CH_KEYS / (4 * RW); ++i) {
-                            const int row = (i * 4 + cwarp) * RW + row0;
+#pragma unroll 4
+                        for (int i = 0; i < CH_KEYS / (C::CW * RW); ++i) {
+                            const int row = (i * C::CW + cwarp) * RW + row0;
                             const uint4 v = *reinterpret_cast<const uint4*>(src + row * D + ch * 16);
                             uint4 o0, o1;
                             if (kv == 0) {
