@@ -81,8 +81,8 @@ struct TCfg {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_LAND = OFF_KV + NS * TILE;
-    static constexpr int OFF_SC = OFF_LAND + LS * CODES;  // [RING][K | V][128] scales
-    static constexpr int OFF_U = OFF_SC + (FP8 ? RING * 2 * CH_KEYS * 4 : 0);
+    static constexpr int OFF_SC = OFF_LAND + LS * CODES;  // [RING][3][128]: K's scales; V's, as log2; 1 / V's
+    static constexpr int OFF_U = OFF_SC + (FP8 ? RING * 3 * CH_KEYS * 4 : 0);
     static constexpr int OFF_CU = OFF_U + (PAGED_MAX_B + 1) * 8;
     static constexpr int OFF_LEN = OFF_CU + (PAGED_MAX_B + 1) * 4;
     static constexpr int OFF_ML = (OFF_LEN + PAGED_MAX_B * 4 + 15) / 16 * 16;  // [2][128] (max, sum)
@@ -97,9 +97,9 @@ struct TCfg {
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + RING * 4 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
-    // Q x K in bf16, or in fp16 with FP8 (formats 0 instead of 1 in bits 7 and 10)
+    // bf16, or fp16 with FP8 (formats 0 instead of 1 in bits 7 and 10)
     static constexpr uint32_t IDESC_S = umma_idesc_bf16(128, CH_STEP) & (FP8 ? ~((1u << 7) | (1u << 10)) : ~0u);
-    static constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D, false, true);
+    static constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D, false, true) & (FP8 ? ~((1u << 7) | (1u << 10)) : ~0u);
 };
 
 // Four E4M3 codes -> fp16 pairs, exactly.
@@ -110,21 +110,24 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
         : "r"(w));
 }
 
-// Four E4M3 codes -> bf16 pairs, exactly, by way of fp16 and fp32: the conversions share their
-// time between two pipes (moving the bits by integer operations and scaling by 2^120 took 4%
-// longer in all).
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi)
+__device__ __forceinline__ float lg2(float x)
 {
-    uint32_t h[2];
-    codes_to_f16(w, h[0], h[1]);
-    asm("{\n\t.reg .b16 a, b;\n\t.reg .f32 x, y;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 x, a;\n\tcvt.f32.f16 y, b;\n\t"
-        "cvt.rn.bf16x2.f32 %0, y, x;\n\t}"
-        : "=r"(lo)
-        : "r"(h[0]));
-    asm("{\n\t.reg .b16 a, b;\n\t.reg .f32 x, y;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 x, a;\n\tcvt.f32.f16 y, b;\n\t"
-        "cvt.rn.bf16x2.f32 %0, y, x;\n\t}"
-        : "=r"(hi)
-        : "r"(h[1]));
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two weights, as the MMAs take them.
+template <bool FP8>
+__device__ __forceinline__ uint32_t pack_weights(float2 w)
+{
+    if constexpr (FP8) {
+        uint32_t h;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(w.y), "f"(w.x));
+        return h;
+    } else {
+        return pack_bf16x2(w.x, w.y);
+    }
 }
 
 // Store of 32 columns x 16 lanes: register 2j of thread t goes to lane t / 4, column 4j + t % 4,
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                                         &land_full[slot], 0, y, z);
                             if (kv == 0 && !bad) {
                                 const long long r = (static_cast<long long>(z) << p.page_shift) + y;
-                                float* dst = s_sc + (it % C::RING) * 2 * CH_KEYS + (box << bp_shift);
+                                float* dst = s_sc + (it % C::RING) * 3 * CH_KEYS + (box << bp_shift);
                                 bulk_load(dst, a.k_scales + r, bp * 4, &land_full[slot]);
                                 bulk_load(dst + CH_KEYS, a.v_scales + r, bp * 4, &land_full[slot]);
                             }
@@ -520,26 +523,26 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                 }
                 if (FP8 && k == 0) {  // (the scores wait for the converted Q rows)
                     const float* qs = s_qs + (n & 1) * CH_ROWS + row0 + (lane >> 2);
-                    // not 0, as that times the -inf of a key out of sight is no number (a tiny or zero row: its
-                    // scores are 0 either way)
-                    sl2a = fmaxf(sl2 * qs[0], 0x1p-126f);
-                    sl2b = fmaxf(sl2 * qs[8], 0x1p-126f);
+                    sl2a = sl2 * qs[0];
+                    sl2b = sl2 * qs[8];
                 }
                 if (active_warp) {
                     const uint32_t bad = s_bad[it % C::RING] >> (4 * hh) & 15u;
-                    const float* ks = s_sc + (it % C::RING) * 2 * CH_KEYS + hh * CH_STEP + q2;
+                    const float* ks = s_sc + (it % C::RING) * 3 * CH_KEYS + hh * CH_STEP + q2;
                     const bool masked = pos_first - kb < CH_STEP - 1 || bad != 0;  // warp-uniform
                     uint32_t sv[32];
                     tmem_ld_16x256b_x8(sp, sv);
                     tmem_wait_ld();
                     tmem_regs_ready(sv);
-                    if constexpr (FP8) {
+                    const float2 sca = make_float2(sl2a, sl2a), scb = make_float2(sl2b, sl2b);
+                    if constexpr (FP8) {  // in log2 units, with the values' scales: s + log2 vs
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float2 f = *reinterpret_cast<const float2*>(ks + 8 * i);
+                            const float2 lv = *reinterpret_cast<const float2*>(ks + CH_KEYS + 8 * i);
                             uint32_t* x = sv + 4 * i;
-                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), f);
-                            const float2 z = __fmul2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), f);
+                            const float2 y = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sca), f, lv);
+                            const float2 z = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), scb), f, lv);
                             x[0] = __float_as_uint(y.x);
                             x[1] = __float_as_uint(y.y);
                             x[2] = __float_as_uint(z.x);
@@ -570,8 +573,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     float mxa = fmaxf(xa[0], xa[1]), mxb = fmaxf(xb[0], xb[1]);
                     mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
                     mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
-                    mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2)) * sl2a;
-                    mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2)) * sl2b;
+                    mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2)) * (FP8 ? 1.f : sl2a);
+                    mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2)) * (FP8 ? 1.f : sl2b);
                     // the reference maximum moves (and O with it, for the warp together) only when the
                     // row's maximum has grown by more than 2^8: the weights stay below 2^8
                     const bool mva = mxa > ma + kRescaleThreshold || ma == -INFINITY;
@@ -604,26 +607,33 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                     // through the hardware unit, where 2^-inf is exactly 0: none / an eighth / a quarter / half of them
                     // as a polynomial on the FMA pipe took 592 / 601 / 607 / 647 us for two 3.5K-token chunks (and none
                     // at all 602: they are hidden behind the products)
-                    const float2 sca = make_float2(sl2a, sl2a), scb = make_float2(sl2b, sl2b);
                     const float mua = ma == -INFINITY ? 0.f : -ma, mub = mb == -INFINITY ? 0.f : -mb;
                     float2 acca = make_float2(0.f, 0.f), accb = acca;
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t* x = sv + 4 * i;
-                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sca, make_float2(mua, mua));
-                        const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), scb, make_float2(mub, mub));
-                        float2 pa = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                        float2 pb = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-                        acca = __fadd2_rn(acca, pa);
-                        accb = __fadd2_rn(accb, pb);
+                        float2 y = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+                        float2 z = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
                         if constexpr (FP8) {
-                            const float2 f = *reinterpret_cast<const float2*>(ks + CH_KEYS + 8 * i);
-                            pa = __fmul2_rn(pa, f);
-                            pb = __fmul2_rn(pb, f);
+                            y = __fadd2_rn(y, make_float2(mua, mua));
+                            z = __fadd2_rn(z, make_float2(mub, mub));
+                        } else {
+                            y = __ffma2_rn(y, sca, make_float2(mua, mua));
+                            z = __ffma2_rn(z, scb, make_float2(mub, mub));
                         }
-                        pk[2 * i] = pack_bf16x2(pa.x, pa.y);
-                        pk[2 * i + 1] = pack_bf16x2(pb.x, pb.y);
+                        const float2 pa = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                        const float2 pb = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+                        if constexpr (FP8) {  // the sums are of the weights without the values' scales
+                            const float2 f = *reinterpret_cast<const float2*>(ks + 2 * CH_KEYS + 8 * i);
+                            acca = __ffma2_rn(pa, f, acca);
+                            accb = __ffma2_rn(pb, f, accb);
+                        } else {
+                            acca = __fadd2_rn(acca, pa);
+                            accb = __fadd2_rn(accb, pb);
+                        }
+                        pk[2 * i] = pack_weights<FP8>(pa);
+                        pk[2 * i + 1] = pack_weights<FP8>(pb);
                     }
                     tmem_st_16x128b_x8(sp, pk);
                     la += acca.x + acca.y;
@@ -734,9 +744,11 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
     } else if (warp >= 20) {
         if constexpr (FP8) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
-            // ===== Q -> fp16 in place; codes -> 16-bit tiles in the 128-byte-swizzled layout: K fp16, V bf16 =====
-            // K's products need no range beyond Q's and the codes', and fp16 is one conversion for two codes; the
-            // weights, times the values' scales, need bf16's.
+            // ===== Q -> fp16 in place; codes -> fp16 tiles in the 128-byte-swizzled layout =====
+            // fp16 is one conversion for two codes, exact, and three more bits of the weights than bf16 (the long
+            // chunk's outputs are off by 0.0017 of their norm, their own rounding, where bf16 weights gave 0.0025).
+            // Its range is enough: Q's rows are scaled into it, and a row's running reference is the maximum of
+            // s + log2 vs over the keys it sees, so its weights times the values' scales stay in (0, 2^8].
             const int tid = threadIdx.x - 640, cwarp = tid >> 5;
             // chunk of 16 codes: two rows by four chunks in eight neighbouring lanes, so that either half of their
             // 32 bytes falls on eight different bank groups
@@ -787,10 +799,16 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                         if (!ok) break;
                         const uint32_t bad = s_bad[it % C::RING];
                         const bool partial = nv < CH_KEYS || bad != 0;
-                        if (kv == 0 && partial && tid < CH_KEYS && (tid >= nv || (bad >> (tid / 16) & 1u))) {
-                            float* sc = s_sc + (it % C::RING) * 2 * CH_KEYS + tid;
-                            sc[0] = 0.f;
-                            sc[CH_KEYS] = 0.f;
+                        if (kv == 0 && tid < CH_KEYS) {
+                            float* sc = s_sc + (it % C::RING) * 3 * CH_KEYS + tid;
+                            // a scale under 2^-100, 0 included, counts as that: its codes times it are next to nothing
+                            float lv = fmaxf(lg2(sc[CH_KEYS]), -100.f);
+                            if (partial && (tid >= nv || (bad >> (tid / 16) & 1u))) {  // no key: anything may stand there
+                                sc[0] = 0.f;
+                                lv = 0.f;
+                            }
+                            sc[CH_KEYS] = lv;
+                            sc[2 * CH_KEYS] = fast_exp2(-lv);
                         }
                         const uint8_t* src = smem + C::OFF_LAND + ls * C::CODES;
                         uint8_t* dst = smem + C::OFF_KV + slot * C::TILE + (ch >> 2) * C::BOX;
@@ -799,18 +817,11 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                             const int row = (i * C::CW + cwarp) * RW + row0;
                             const uint4 v = *reinterpret_cast<const uint4*>(src + row * D + ch * 16);
                             uint4 o0, o1;
-                            if (kv == 0) {
-                                codes_to_f16(v.x, o0.x, o0.y);
-                                codes_to_f16(v.y, o0.z, o0.w);
-                                codes_to_f16(v.z, o1.x, o1.y);
-                                codes_to_f16(v.w, o1.z, o1.w);
-                            } else {
-                                codes_to_bf16(v.x, o0.x, o0.y);
-                                codes_to_bf16(v.y, o0.z, o0.w);
-                                codes_to_bf16(v.z, o1.x, o1.y);
-                                codes_to_bf16(v.w, o1.z, o1.w);
-                                if (partial && row >= nv) o0 = o1 = make_uint4(0, 0, 0, 0);
-                            }
+                            codes_to_f16(v.x, o0.x, o0.y);
+                            codes_to_f16(v.y, o0.z, o0.w);
+                            codes_to_f16(v.z, o1.x, o1.y);
+                            codes_to_f16(v.w, o1.z, o1.w);
+                            if (kv == 1 && partial && row >= nv) o0 = o1 = make_uint4(0, 0, 0, 0);
                             *reinterpret_cast<uint4*>(dst + swz128(row, 2 * ch0)) = o0;
                             *reinterpret_cast<uint4*>(dst + swz128(row, 2 * ch0 + 1)) = o1;
                         }
