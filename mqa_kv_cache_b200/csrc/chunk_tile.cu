@@ -17,10 +17,10 @@
 // time of a thread per row, which the chain scores - softmax - P V - next scores waits for),
 // 16 issues the scores' MMAs, 18 the values', 17 loads K/V pages (one box per page and
 // 64-column half, page entries fetched one tile ahead), 19 hands out the pieces and loads Q.  FP8: warps 20-27 turn the
-// codes of each landed tile into bf16 (exact) in the layout that the MMAs read; the keys'
-// scales multiply the scores and the values' scales the weights, in fp32.
+// codes of each landed tile into fp16 (exact) in the layout that the MMAs read; the keys'
+// scales multiply the scores, and the values' scales join them as logarithms, in fp32.
 // TMEM: S0 | S1 | O0 | O1.  Scores are computed 64 keys at a time in either half of their 128
-// columns, one step ahead of the softmax; the weights (bf16) overwrite the first half of
+// columns, one step ahead of the softmax; the weights (16 bits) overwrite the first half of
 // their scores and the P V product takes them from there.  (128 keys at a time, where the
 // next scores wait for the P V that reads the weights in their place, the chain scores -
 // softmax - P V took 3960 cycles a tile against 2050 of the products alone.)
@@ -38,7 +38,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: the maximum moves only when it grows by more than 2^8
 
-// A stretch of one unit's key tiles, as warp 11 hands it to the others (rows = 0: no more).
+// A stretch of one unit's key tiles, as warp 19 hands it to the others (rows = 0: no more).
 struct Piece {
     int b, kvh;
     int tok0;    // the block's first packed token
@@ -64,22 +64,26 @@ __device__ __forceinline__ int piece_steps(const P& u, int t)
     return (upto(u.keys) + 1 - t) >> 1;
 }
 
-template <int D, bool FP8>
+// QT: the most Q tiles that a block of the call can have.  The room of the second one holds more of K/V where
+// there is none (16 x 8 tokens over 8K rows, one tile / two: bf16 95.8 / 97.2 us, FP8 104.8 / 110.9; 2 x 9 over
+// 300: 13.8 / 14.3, 17.1 / 17.9).
+template <int D, bool FP8, int QT>
 struct TCfg {
     static constexpr int HALVES = D / 64;
     static constexpr int BOX = CH_KEYS * 128;          // 128 rows x 64 bf16
     static constexpr int TILE = HALVES * BOX;          // a Q, K or V tile
     static constexpr int CODES = CH_KEYS * D;          // a tile's codes
-    static constexpr int NS = (FP8 ? 3 : 4) * 2 / HALVES;  // bf16 K/V slots
-    static constexpr int LS = FP8 ? 4 / HALVES : 0;        // code slots
-    static constexpr int RING = 8;                     // tiles whose page flags (and scales) are kept
-    // Warps that widen codes.  8 (40 registers each) against 4 (64): 16 x 8 tokens over 8K rows 113 / 131 us, four
-    // 2K prompts 278 / 303, 2 x 40 tokens 20 / 23.5, but 1021 tokens over 31K rows on one KV head 1164 / 1090 (there
-    // they wait for the softmax, and take its issue slots).
+    static constexpr int NS = (FP8 ? 3 : 6 - QT) * 2 / HALVES;                    // 16-bit K/V slots
+    static constexpr int LS = !FP8 ? 0 : QT == 2 ? 4 / HALVES : D == 128 ? 4 : 6;  // code slots
+    static constexpr int RING = 8;  // tiles whose page flags (and scales) are kept: the loads run up to 6 ahead of the softmax
+    // Warps that widen codes.  8 (40 registers each) against 4 (64): 16 x 8 tokens over 8K rows 111 / 122 us, four
+    // 2K prompts 278 / 312, 2 x 40 tokens 20 / 22.2, but 1021 tokens over 31K rows on one KV head 1170 / 1140 (there
+    // they wait for the softmax, and take its issue slots).  All of them on one tile: with half on K's and half
+    // on V's, a tile takes longer to come (117 us, 298, 20.4, 1249).
     static constexpr int CW = FP8 ? 8 : 0;
     static constexpr int THREADS = 640 + 32 * CW;
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int OFF_KV = QT * TILE;
     static constexpr int OFF_LAND = OFF_KV + NS * TILE;
     static constexpr int OFF_SC = OFF_LAND + LS * CODES;  // [RING][3][128]: K's scales; V's, as log2; 1 / V's
     static constexpr int OFF_U = OFF_SC + (FP8 ? RING * 3 * CH_KEYS * 4 : 0);
@@ -200,12 +204,12 @@ __device__ __forceinline__ void commit_to(uint32_t elect, uint64_t* bar)
         : "memory");
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
+template <int D, bool FP8, int QT>
+__global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
     chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, ChunkArgs a)
 {
-    using C = TCfg<D, FP8>;
+    using C = TCfg<D, FP8, QT>;
     constexpr int NS = C::NS, LS = C::LS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (stays a shared-memory address to the compiler)
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         Piece u;
         for (int np = 0; ok && take(np, u); ++np) {
             ok = ready(FP8 ? q_ready : q_full, np & 1, s_abort);
-            const bool pair = u.qt == 2;
+            const bool pair = QT == 2 && u.qt == 2;
             const int n0 = piece_steps(u, 0), n1 = piece_steps(u, 1), n = max(n0, n1);
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
         uint32_t gn[2] = {0, 0};
         Piece u;
         for (int np = 0; ok && take(np, u); ++np) {
-            const bool pair = u.qt == 2;
+            const bool pair = QT == 2 && u.qt == 2;
             const int n0 = piece_steps(u, 0), n1 = piece_steps(u, 1), n = max(n0, n1);
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
             const volatile Piece& u = s_piece[n % PIECES];
             if (u.rows == 0) break;
             const int tb = u.tb;
-            const bool pair = u.qt == 2;  // two Q tiles; else one, its keys dealt out in steps
+            const bool pair = QT == 2 && u.qt == 2;  // two Q tiles; else one, its keys dealt out in steps
             const int row0 = (pair ? t * 128 : 0) + r16;  // the warp's first row of the block
             const int pos_first = u.pos0 + (row0 >> gs);
             const bool active_warp = row0 < u.rows;
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::THREADS, 1)
                         ma = na;
                         mb = nb;
                     }
-                    // weights 2^(s sl2 - m), to TMEM as bf16 over the scores' first half.  Every exponential goes
+                    // weights 2^(s sl2 - m), to TMEM over the scores' first half.  Every exponential goes
                     // through the hardware unit, where 2^-inf is exactly 0: none / an eighth / a quarter / half of them
                     // as a polynomial on the FMA pipe took 592 / 601 / 607 / 647 us for two 3.5K-token chunks (and none
                     // at all 602: they are hidden behind the products)
@@ -964,7 +968,7 @@ __global__ void __launch_bounds__(TM_WARPS * 32) chunk_tile_merge_kernel(ChunkAr
     if (lane == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int QT>
 cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                          int num_sms, cudaStream_t stream)
 {
@@ -973,16 +977,24 @@ cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& tm_q, const CUte
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(chunk_tile_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<D, FP8>::SMEM);
+        e = cudaFuncSetAttribute(chunk_tile_kernel<D, FP8, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<D, FP8, QT>::SMEM);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
     const int grid = num_sms < CHUNK_MAX_CTAS ? num_sms : CHUNK_MAX_CTAS;
-    e = launch_pdl(chunk_tile_kernel<D, FP8>, dim3(grid), dim3(TCfg<D, FP8>::THREADS), TCfg<D, FP8>::SMEM, stream, tm_q,
+    e = launch_pdl(chunk_tile_kernel<D, FP8, QT>, dim3(grid), dim3(TCfg<D, FP8, QT>::THREADS), TCfg<D, FP8, QT>::SMEM, stream, tm_q,
                    tm_k, tm_v, a);
     if (e != cudaSuccess) return e;
     const int rows = a.max_q < CH_ROWS / a.g ? a.max_q * a.g : CH_ROWS;
     return launch_pdl(chunk_tile_merge_kernel<D>, dim3(grid, (rows + TM_WARPS - 1) / TM_WARPS), dim3(TM_WARPS * 32), 0, stream, a);
+}
+
+template <int D, bool FP8>
+cudaError_t launch_tiles(const ChunkArgs& a, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                         int num_sms, cudaStream_t stream)
+{
+    return a.max_q * a.g <= CH_ROWS / 2 ? launch_typed<D, FP8, 1>(a, tm_q, tm_k, tm_v, num_sms, stream)
+                                        : launch_typed<D, FP8, 2>(a, tm_q, tm_k, tm_v, num_sms, stream);
 }
 
 }  // namespace
@@ -991,10 +1003,10 @@ cudaError_t launch_chunk_tile(const ChunkArgs& a, bool fp8, const CUtensorMap& t
                               const CUtensorMap& tm_v, int num_sms, cudaStream_t stream)
 {
     if (a.d == 128)
-        return fp8 ? launch_typed<128, true>(a, tm_q, tm_k, tm_v, num_sms, stream)
-                   : launch_typed<128, false>(a, tm_q, tm_k, tm_v, num_sms, stream);
-    return fp8 ? launch_typed<64, true>(a, tm_q, tm_k, tm_v, num_sms, stream)
-               : launch_typed<64, false>(a, tm_q, tm_k, tm_v, num_sms, stream);
+        return fp8 ? launch_tiles<128, true>(a, tm_q, tm_k, tm_v, num_sms, stream)
+                   : launch_tiles<128, false>(a, tm_q, tm_k, tm_v, num_sms, stream);
+    return fp8 ? launch_tiles<64, true>(a, tm_q, tm_k, tm_v, num_sms, stream)
+               : launch_tiles<64, false>(a, tm_q, tm_k, tm_v, num_sms, stream);
 }
 
 }  // namespace kvattn
