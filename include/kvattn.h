@@ -481,8 +481,8 @@ int attn_decode_sparse_fp8(const kvattn_bf16* q, const uint8_t* latent_fp8, cons
  * Device-side checks.  cu outside 0 .. n_tokens or decreasing, or a length outside
  * [0, max_pages * page_size]: forced into range, KVATTN_STATUS_BAD_LENGTH.  A needed page
  * outside [0, n_pages): its rows are skipped, KVATTN_STATUS_BAD_INDEX.  Sequences that
- * overlap in cu, or share a page that an append writes, give undefined values (never
- * stray accesses).
+ * overlap in cu, or share a page that an append writes, or hold it twice, give undefined
+ * values (never stray accesses).
  * Limits: 1 <= B <= 1024, head_dim 64 or 128, page_size a power of two in 16 .. 1024,
  * max_pages * page_size <= 2^30, n_tokens * heads < 2^31, n_pages * n_kv_head < 2^31,
  * B * n_kv_head <= 16384.
@@ -525,10 +525,11 @@ int kv_read_paged_fp8(const uint8_t* k_codes, const float* k_scales, const uint8
  * attn_chunk_paged: attention of every new token over rows 0 .. its own position of its
  * sequence (the new tokens' rows having been appended): out [n_tokens][n_head][d] bf16 =
  * softmax(scale q k^T) v, lse [n_tokens][n_head] fp32 (natural log) or NULL, query head h
- * reading KV head h / g.  q is rotated by the caller (rope_apply_qk).  A token that sees
- * no row (seq_lens[b] < n_b, or every page skipped) gets out = 0 and lse = -inf.  Rows
- * past a sequence's length are never used, whatever they hold; its own rows must be finite
- * (a non-finite value row can reach the queries that share a key tile with it).
+ * reading KV head h / g; neither may overlap an input.  q is rotated by the caller
+ * (rope_apply_qk).  A token that sees no row (seq_lens[b] < n_b, or every page skipped)
+ * gets out = 0 and lse = -inf.  Rows past a sequence's length are never used, whatever they
+ * hold; its own rows must be finite (a non-finite value row can reach the queries that
+ * share a key tile with it).
  * max_q: an upper bound of the chunk lengths that the host knows (<= 0: n_tokens); it
  * decides how the work is laid out.  A chunk longer than max_q sets
  * KVATTN_STATUS_BAD_LENGTH and its tokens from max_q on are left unwritten.
@@ -537,9 +538,9 @@ int kv_read_paged_fp8(const uint8_t* k_codes, const float* k_scales, const uint8
  * the first call on it, and every call leaves them zero except one that sets
  * KVATTN_STATUS_TIMEOUT.  Calls that share a workspace must be ordered.
  * Supported: g = n_head / n_kv_head in {1, 2, 4, 8, 16, 32, 64}.
- * attn_chunk_paged_fp8: the same over an FP8 cache.  The codes enter the products exactly;
- * the keys' scales multiply the scores and the values' scales the weights, in fp32, so the
- * dequantised rows are never rounded.
+ * attn_chunk_paged_fp8: the same over an FP8 cache.  The codes enter the products exactly, as
+ * fp16; the keys' scales multiply the scores and the values' scales the weights, in fp32, so
+ * the dequantised rows are never rounded.
  */
 size_t attn_chunk_paged_workspace_bytes(int B, int n_tokens, int max_q, int n_head, int n_kv_head, int head_dim);
 

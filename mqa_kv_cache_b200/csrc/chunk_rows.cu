@@ -163,13 +163,13 @@ __device__ void join_pieces(const ChunkArgs& a, int gs, int f, int i0, int i1, i
             for (int k = 0; k < RGROUP; ++k) Mn = fmaxf(Mn, ml[k].x);
             const float mu = Mn == -INFINITY ? 0.f : Mn;
             const float c = fast_exp2(M - mu);
-            L *= c;
+            L = sum_exp2(L, M - mu);
             acc = make_float4(acc.x * c, acc.y * c, acc.z * c, acc.w * c);
             M = Mn;
 #pragma unroll
             for (int k = 0; k < RGROUP; ++k) {
                 const float e = fast_exp2(ml[k].x - mu);
-                L += e * ml[k].y;
+                L += sum_exp2(ml[k].y, ml[k].x - mu);
                 acc.x += e * o[k].x;
                 acc.y += e * o[k].y;
                 acc.z += e * o[k].z;
@@ -572,9 +572,8 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
                             float x = sc[n][i][e] * (FP8 ? qs[n][e & 1] * ks[i][e >> 1] : sl2);
                             if (masked && ((bad >> i & 1u) || t * RK + tok0 + i * 16 + (e >> 1) * 8 + r0 > pos[n][e & 1])) x = -INFINITY;
                             sc[n][i][e] = x;
-                            // FP8: the sums use the same reference as the weighted values: it may lie below the
-                            // largest score (rows of tiny scale), but by no more than fp32 holds
-                            mx[n][e & 1] = fmaxf(mx[n][e & 1], FP8 ? fmaxf(x + lv[i][e >> 1], x - 100.f) : x);
+                            // FP8: the sums use the same reference as the weighted values
+                            mx[n][e & 1] = fmaxf(mx[n][e & 1], FP8 ? fmaxf(x + lv[i][e >> 1], x + CHUNK_MIN_LOG2_VS) : x);
                         }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -592,7 +591,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
                         for (int e = 0; e < 2; ++e) {
                             const float mn = fmaxf(m[n][e], mx[n][e]);
                             al[e] = m[n][e] == -INFINITY ? 0.f : fast_exp2(m[n][e] - mn);
-                            l[n][e] *= al[e];
+                            if (m[n][e] != -INFINITY) l[n][e] = sum_exp2(l[n][e], m[n][e] - mn);
                             m[n][e] = mn;
                         }
 #pragma unroll
@@ -701,7 +700,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
                 for (int j = 0; j < 4; ++j) M = fmaxf(M, ml[j * WR].x);
                 const float mu = M == -INFINITY ? 0.f : M;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) L += fast_exp2(ml[j * WR].x - mu) * ml[j * WR].y;
+                for (int j = 0; j < 4; ++j) L += sum_exp2(ml[j * WR].y, ml[j * WR].x - mu);
                 const float w = fast_exp2(m[n][e] - mu);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {

@@ -18,7 +18,7 @@
 // 16 issues the scores' MMAs, 18 the values', 17 loads K/V pages (one box per page and
 // 64-column half, page entries fetched one tile ahead), 19 hands out the pieces and loads Q.  FP8: warps 20-27 turn the
 // codes of each landed tile into fp16 (exact) in the layout that the MMAs read; the keys'
-// scales multiply the scores, and the values' scales join them as logarithms, in fp32.
+// scales multiply the scores and the values' scales the weights, in fp32.
 // TMEM: S0 | S1 | O0 | O1.  Scores are computed 64 keys at a time in either half of their 128
 // columns, one step ahead of the softmax; the weights (16 bits) overwrite the first half of
 // their scores and the P V product takes them from there.  (128 keys at a time, where the
@@ -85,7 +85,7 @@ struct TCfg {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_KV = QT * TILE;
     static constexpr int OFF_LAND = OFF_KV + NS * TILE;
-    static constexpr int OFF_SC = OFF_LAND + LS * CODES;  // [RING][3][128]: K's scales; V's, as log2; 1 / V's
+    static constexpr int OFF_SC = OFF_LAND + LS * CODES;  // [RING][3][128]: K's scales; V's, as log2; V's
     static constexpr int OFF_U = OFF_SC + (FP8 ? RING * 3 * CH_KEYS * 4 : 0);
     static constexpr int OFF_CU = OFF_U + (PAGED_MAX_B + 1) * 8;
     static constexpr int OFF_LEN = OFF_CU + (PAGED_MAX_B + 1) * 4;
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
                                 const long long r = (static_cast<long long>(z) << p.page_shift) + y;
                                 float* dst = s_sc + (it % C::RING) * 3 * CH_KEYS + (box << bp_shift);
                                 bulk_load(dst, a.k_scales + r, bp * 4, &land_full[slot]);
-                                bulk_load(dst + CH_KEYS, a.v_scales + r, bp * 4, &land_full[slot]);
+                                bulk_load(dst + 2 * CH_KEYS, a.v_scales + r, bp * 4, &land_full[slot]);
                             }
                         }
                     } else {
@@ -527,8 +527,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
                 }
                 if (FP8 && k == 0) {  // (the scores wait for the converted Q rows)
                     const float* qs = s_qs + (n & 1) * CH_ROWS + row0 + (lane >> 2);
-                    sl2a = sl2 * qs[0];
-                    sl2b = sl2 * qs[8];
+                    // not 0, as that times the -inf of a key out of sight is no number (a tiny or zero row: its
+                    // scores are 0 either way)
+                    sl2a = fmaxf(sl2 * qs[0], 0x1p-126f);
+                    sl2b = fmaxf(sl2 * qs[8], 0x1p-126f);
                 }
                 if (active_warp) {
                     const uint32_t bad = s_bad[it % C::RING] >> (4 * hh) & 15u;
@@ -539,14 +541,13 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
                     tmem_wait_ld();
                     tmem_regs_ready(sv);
                     const float2 sca = make_float2(sl2a, sl2a), scb = make_float2(sl2b, sl2b);
-                    if constexpr (FP8) {  // in log2 units, with the values' scales: s + log2 vs
+                    if constexpr (FP8) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float2 f = *reinterpret_cast<const float2*>(ks + 8 * i);
-                            const float2 lv = *reinterpret_cast<const float2*>(ks + CH_KEYS + 8 * i);
                             uint32_t* x = sv + 4 * i;
-                            const float2 y = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sca), f, lv);
-                            const float2 z = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), scb), f, lv);
+                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), f);
+                            const float2 z = __fmul2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), f);
                             x[0] = __float_as_uint(y.x);
                             x[1] = __float_as_uint(y.y);
                             x[2] = __float_as_uint(z.x);
@@ -571,8 +572,15 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t* x = sv + 4 * i;
-                        xa[i & 1] = fmax3(xa[i & 1], __uint_as_float(x[0]), __uint_as_float(x[1]));
-                        xb[i & 1] = fmax3(xb[i & 1], __uint_as_float(x[2]), __uint_as_float(x[3]));
+                        float2 y = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+                        float2 z = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
+                        if constexpr (FP8) {  // the maximum of s + log2 vs, in log2 units
+                            const float2 lv = *reinterpret_cast<const float2*>(ks + CH_KEYS + 8 * i);
+                            y = __ffma2_rn(y, sca, lv);
+                            z = __ffma2_rn(z, scb, lv);
+                        }
+                        xa[i & 1] = fmax3(xa[i & 1], y.x, y.y);
+                        xb[i & 1] = fmax3(xb[i & 1], z.x, z.y);
                     }
                     float mxa = fmaxf(xa[0], xa[1]), mxb = fmaxf(xb[0], xb[1]);
                     mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
@@ -588,8 +596,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
                         const bool rsa = mva && ma != -INFINITY, rsb = mvb && mb != -INFINITY;
                         if (__any_sync(0xffffffffu, rsa || rsb)) {
                             const float ala = rsa ? fast_exp2(ma - na) : 1.f, alb = rsb ? fast_exp2(mb - nb) : 1.f;
-                            la *= ala;
-                            lb *= alb;
+                            if (rsa) la = sum_exp2(la, ma - na);
+                            if (rsb) lb = sum_exp2(lb, mb - nb);
                             // O must be still: the P V of the step before has finished
                             if (!ready(&pv_done[2 * t + ((cnt - 1) & 1)], ((cnt - 1) >> 1) & 1, s_abort)) continue;
                             tc_fence_after();
@@ -617,24 +625,16 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t* x = sv + 4 * i;
-                        float2 y = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
-                        float2 z = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
+                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sca, make_float2(mua, mua));
+                        const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), scb, make_float2(mub, mub));
+                        float2 pa = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                        float2 pb = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+                        acca = __fadd2_rn(acca, pa);
+                        accb = __fadd2_rn(accb, pb);
                         if constexpr (FP8) {
-                            y = __fadd2_rn(y, make_float2(mua, mua));
-                            z = __fadd2_rn(z, make_float2(mub, mub));
-                        } else {
-                            y = __ffma2_rn(y, sca, make_float2(mua, mua));
-                            z = __ffma2_rn(z, scb, make_float2(mub, mub));
-                        }
-                        const float2 pa = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                        const float2 pb = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-                        if constexpr (FP8) {  // the sums are of the weights without the values' scales
                             const float2 f = *reinterpret_cast<const float2*>(ks + 2 * CH_KEYS + 8 * i);
-                            acca = __ffma2_rn(pa, f, acca);
-                            accb = __ffma2_rn(pb, f, accb);
-                        } else {
-                            acca = __fadd2_rn(acca, pa);
-                            accb = __fadd2_rn(accb, pb);
+                            pa = __fmul2_rn(pa, f);
+                            pb = __fmul2_rn(pb, f);
                         }
                         pk[2 * i] = pack_weights<FP8>(pa);
                         pk[2 * i + 1] = pack_weights<FP8>(pb);
@@ -677,8 +677,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
                 ub = fast_exp2(mb - fb);
                 va = fast_exp2(oa.x - fa);
                 vb = fast_exp2(ob.x - fb);
-                la = ua * la + va * oa.y;
-                lb = ub * lb + vb * ob.y;
+                la = sum_exp2(la, ma - fa) + sum_exp2(oa.y, oa.x - fa);
+                lb = sum_exp2(lb, mb - fb) + sum_exp2(ob.y, ob.x - fb);
                 ma = Ma;
                 mb = Mb;
                 c0 = t * (D / 32);
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
             // fp16 is one conversion for two codes, exact, and three more bits of the weights than bf16 (the long
             // chunk's outputs are off by 0.0017 of their norm, their own rounding, where bf16 weights gave 0.0025).
             // Its range is enough: Q's rows are scaled into it, and a row's running reference is the maximum of
-            // s + log2 vs over the keys it sees, so its weights times the values' scales stay in (0, 2^8].
+            // s + log2 vs over the keys it sees, so its weights times the values' scales stay below 2^8 (and the largest above 1).
             const int tid = threadIdx.x - 640, cwarp = tid >> 5;
             // chunk of 16 codes: two rows by four chunks in eight neighbouring lanes, so that either half of their
             // 32 bytes falls on eight different bank groups
@@ -805,14 +805,12 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
                         const bool partial = nv < CH_KEYS || bad != 0;
                         if (kv == 0 && tid < CH_KEYS) {
                             float* sc = s_sc + (it % C::RING) * 3 * CH_KEYS + tid;
-                            // a scale under 2^-100, 0 included, counts as that: its codes times it are next to nothing
-                            float lv = fmaxf(lg2(sc[CH_KEYS]), -100.f);
+                            float lv = fmaxf(lg2(sc[2 * CH_KEYS]), CHUNK_MIN_LOG2_VS);
                             if (partial && (tid >= nv || (bad >> (tid / 16) & 1u))) {  // no key: anything may stand there
-                                sc[0] = 0.f;
+                                sc[0] = sc[2 * CH_KEYS] = 0.f;
                                 lv = 0.f;
                             }
                             sc[CH_KEYS] = lv;
-                            sc[2 * CH_KEYS] = fast_exp2(-lv);
                         }
                         const uint8_t* src = smem + C::OFF_LAND + ls * C::CODES;
                         uint8_t* dst = smem + C::OFF_KV + slot * C::TILE + (ch >> 2) * C::BOX;
@@ -936,12 +934,13 @@ __global__ void __launch_bounds__(TM_WARPS * 32) chunk_tile_merge_kernel(ChunkAr
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, o));
         const float mu = Mn == -INFINITY ? 0.f : Mn, c = fast_exp2(M - mu);
+        L = sum_exp2(L, M - mu);
         M = Mn;
         const float wl = fast_exp2(ml.x - mu);
-        float sum = wl * ml.y;
+        float sum = sum_exp2(ml.y, ml.x - mu);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        L = L * c + sum;
+        L += sum;
 #pragma unroll
         for (int k = 0; k < PL; ++k) acc[k] *= c;
         for (int i = 0; i < n; i += BATCH) {

@@ -97,6 +97,17 @@ __host__ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& p, int 
     return s;
 }
 
+// FP8: a row's running reference is the maximum of s + max(log2 vs, this): a tiny or zero value row does not
+// lower it further, so that its weight without vs, up to 2^96 of the reference, and sums of those fit fp32.
+constexpr float CHUNK_MIN_LOG2_VS = -96.f;
+
+// l 2^x for a sum l of weights that may be that large, and x that far below 0: 2^x alone may underflow.
+__device__ __forceinline__ float sum_exp2(float l, float x)
+{
+    const float h = fast_exp2(0.5f * x);
+    return l * h * h;
+}
+
 // E4M3 codes -> fp32, two at a time (every code is exact in fp16 and fp32).
 __device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t codes)
 {

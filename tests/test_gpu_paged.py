@@ -354,6 +354,22 @@ def test_fp8_queries_of_any_size(K, n, e):
     R.check(out, lse, R.attention(q, cu, lens, table, page, kd, vd, scale, fp16_weights=True), f"2^{e}")
 
 
+@pytest.mark.parametrize("e", [-80, 0, 80])
+@pytest.mark.parametrize("n", [1, 40, 90])
+def test_fp8_values_of_any_size(K, n, e):
+    """Value rows around 2^e, e^3 apart (one standard deviation), every seventh zero: their scales enter the
+    running reference as logarithms, and a zero row still takes its share of the sum."""
+    page, d, H, Hk, ctx = 32, 128, 4, 2, 400
+    cu, lens, table, n_pages = R.batch([n], [ctx], page, 230)
+    (kc, ks, vc, vs), kd, vd = _cache(n_pages, Hk, page, d, True, 231, spread=3.0)
+    vs *= 2.0 ** e
+    vd = vd * 2.0 ** e
+    vc[:, :, ::7], vs[:, :, ::7], vd[:, :, ::7] = 0, 0.0, 0.0
+    q = _q(n, H, d, 232, 0.3)
+    out, lse = K.attn_chunk_paged_fp8(q.cuda(), *_cuda(cu, lens, table), kc, ks, vc, vs, d ** -0.5, max_q=n)
+    R.check(out, lse, R.attention(q, cu, lens, table, page, kd, vd, d ** -0.5, fp16_weights=True), f"2^{e}")
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_without_a_bound_on_the_chunks(K, fp8):
     assert _case(K, [1, 1, 1], [100, 30, 0], 8, 2, 128, 16, fp8, max_q=None) == 0
