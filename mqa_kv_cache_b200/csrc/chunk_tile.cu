@@ -16,9 +16,10 @@
 // Warps: 0-7 / 8-15 softmax of the two buffers (16 rows a warp, 64 scores a thread: half the
 // time of a thread per row, which the chain scores - softmax - P V - next scores waits for),
 // 16 issues the scores' MMAs, 18 the values', 17 loads K/V pages (one box per page and
-// 64-column half, page entries fetched one tile ahead), 19 hands out the pieces and loads Q.  FP8: warps 20-27 turn the
-// codes of each landed tile into fp16 (exact) in the layout that the MMAs read; the keys'
-// scales multiply the scores and the values' scales the weights, in fp32.
+// 64-column half, page entries fetched one tile ahead), 19 hands out the pieces and loads Q.
+// FP8: warps 20-27, or 20-23, turn the codes of each landed tile into fp16 (exact) in the
+// layout that the MMAs read; the keys' scales multiply the scores and the values' scales
+// the weights, in fp32.
 // TMEM: S0 | S1 | O0 | O1.  Scores are computed 64 keys at a time in either half of their 128
 // columns, one step ahead of the softmax; the weights (16 bits) overwrite the first half of
 // their scores and the P V product takes them from there.  (128 keys at a time, where the
@@ -36,7 +37,9 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: the maximum moves only when it grows by more than 2^8
+// log2 units: the maximum moves only when it grows by more than this (FP8 weights of up to 2^12 fit fp16; at 8, where
+// the values' scales moved it more often, 16 x 8 tokens over 8K rows took 110 us instead of 107)
+constexpr float kRescaleThreshold = 12.0f;
 
 // A stretch of one unit's key tiles, as warp 19 hands it to the others (rows = 0: no more).
 struct Piece {
@@ -67,7 +70,10 @@ __device__ __forceinline__ int piece_steps(const P& u, int t)
 // QT: the most Q tiles that a block of the call can have.  The room of the second one holds more of K/V where
 // there is none (16 x 8 tokens over 8K rows, one tile / two: bf16 95.8 / 97.2 us, FP8 104.8 / 110.9; 2 x 9 over
 // 300: 13.8 / 14.3, 17.1 / 17.9).
-template <int D, bool FP8, int QT>
+// WIDE: the warps that widen codes, 8 (40 registers each) or 4 (64); see launch_tiles.  All of them work on one
+// tile: with half on K's and half on V's, a tile takes longer to come (16 x 8 tokens over 8K rows 117 us against
+// 105, four 2K prompts 298 against 278).
+template <int D, bool FP8, int QT, int WIDE>
 struct TCfg {
     static constexpr int HALVES = D / 64;
     static constexpr int BOX = CH_KEYS * 128;          // 128 rows x 64 bf16
@@ -76,11 +82,7 @@ struct TCfg {
     static constexpr int NS = (FP8 ? 3 : 6 - QT) * 2 / HALVES;                    // 16-bit K/V slots
     static constexpr int LS = !FP8 ? 0 : QT == 2 ? 4 / HALVES : D == 128 ? 4 : 6;  // code slots
     static constexpr int RING = 8;  // tiles whose page flags (and scales) are kept: the loads run up to 6 ahead of the softmax
-    // Warps that widen codes.  8 (40 registers each) against 4 (64): 16 x 8 tokens over 8K rows 111 / 122 us, four
-    // 2K prompts 278 / 312, 2 x 40 tokens 20 / 22.2, but 1021 tokens over 31K rows on one KV head 1170 / 1140 (there
-    // they wait for the softmax, and take its issue slots).  All of them on one tile: with half on K's and half
-    // on V's, a tile takes longer to come (117 us, 298, 20.4, 1249).
-    static constexpr int CW = FP8 ? 8 : 0;
+    static constexpr int CW = FP8 ? WIDE : 0;
     static constexpr int THREADS = 640 + 32 * CW;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_KV = QT * TILE;
@@ -204,12 +206,12 @@ __device__ __forceinline__ void commit_to(uint32_t elect, uint64_t* bar)
         : "memory");
 }
 
-template <int D, bool FP8, int QT>
-__global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
+template <int D, bool FP8, int QT, int WIDE>
+__global__ void __launch_bounds__(TCfg<D, FP8, QT, WIDE>::THREADS, 1)
     chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, ChunkArgs a)
 {
-    using C = TCfg<D, FP8, QT>;
+    using C = TCfg<D, FP8, QT, WIDE>;
     constexpr int NS = C::NS, LS = C::LS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (stays a shared-memory address to the compiler)
@@ -475,7 +477,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
         mbar_wait(done, 0);
         __syncwarp();
     } else if (warp < 16) {
-        // registers: 640 threads at 96 = 512 x 104 + 128 x 64; with FP8 896 at 72 >= 512 x 88 + 128 x 64 + 256 x 40
+        // registers: 640 threads at 96 = 512 x 104 + 128 x 64; with FP8 896 at 72 >= 512 x 88 + 128 x 64 + 256 x 40,
+        // or 768 at 80 = 512 x 88 + 128 x 64 + 128 x 64
         if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;" ::: "memory");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
         // ===== softmax + epilogue: warps 0-7 buffer 0, warps 8-15 buffer 1, 16 rows each =====
@@ -588,16 +591,17 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
                     mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2)) * (FP8 ? 1.f : sl2a);
                     mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2)) * (FP8 ? 1.f : sl2b);
                     // the reference maximum moves (and O with it, for the warp together) only when the
-                    // row's maximum has grown by more than 2^8: the weights stay below 2^8
+                    // row's maximum has grown by more than 2^12: the weights stay below that
                     const bool mva = mxa > ma + kRescaleThreshold || ma == -INFINITY;
                     const bool mvb = mxb > mb + kRescaleThreshold || mb == -INFINITY;
                     if (__any_sync(0xffffffffu, mva || mvb)) {
                         const float na = mva ? fmaxf(mxa, ma) : ma, nb = mvb ? fmaxf(mxb, mb) : mb;
                         const bool rsa = mva && ma != -INFINITY, rsb = mvb && mb != -INFINITY;
                         if (__any_sync(0xffffffffu, rsa || rsb)) {
-                            const float ala = rsa ? fast_exp2(ma - na) : 1.f, alb = rsb ? fast_exp2(mb - nb) : 1.f;
-                            if (rsa) la = sum_exp2(la, ma - na);
-                            if (rsb) lb = sum_exp2(lb, mb - nb);
+                            const float da = rsa ? ma - na : 0.f, db = rsb ? mb - nb : 0.f;
+                            const float ala = fast_exp2(da), alb = fast_exp2(db);
+                            la = sum_exp2(la, da);
+                            lb = sum_exp2(lb, db);
                             // O must be still: the P V of the step before has finished
                             if (!ready(&pv_done[2 * t + ((cnt - 1) & 1)], ((cnt - 1) >> 1) & 1, s_abort)) continue;
                             tc_fence_after();
@@ -747,12 +751,12 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT>::THREADS, 1)
         }
     } else if (warp >= 20) {
         if constexpr (FP8) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(WIDE == 8 ? 40 : 64) : "memory");
             // ===== Q -> fp16 in place; codes -> fp16 tiles in the 128-byte-swizzled layout =====
             // fp16 is one conversion for two codes, exact, and three more bits of the weights than bf16 (the long
             // chunk's outputs are off by 0.0017 of their norm, their own rounding, where bf16 weights gave 0.0025).
             // Its range is enough: Q's rows are scaled into it, and a row's running reference is the maximum of
-            // s + log2 vs over the keys it sees, so its weights times the values' scales stay below 2^8 (and the largest above 1).
+            // s + log2 vs over the keys it sees, so its weights times the values' scales stay below 2^12 (and the largest above 1).
             const int tid = threadIdx.x - 640, cwarp = tid >> 5;
             // chunk of 16 codes: two rows by four chunks in eight neighbouring lanes, so that either half of their
             // 32 bytes falls on eight different bank groups
@@ -967,7 +971,7 @@ __global__ void __launch_bounds__(TM_WARPS * 32) chunk_tile_merge_kernel(ChunkAr
     if (lane == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
 }
 
-template <int D, bool FP8, int QT>
+template <int D, bool FP8, int QT, int WIDE>
 cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                          int num_sms, cudaStream_t stream)
 {
@@ -976,12 +980,12 @@ cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& tm_q, const CUte
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(chunk_tile_kernel<D, FP8, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<D, FP8, QT>::SMEM);
+        e = cudaFuncSetAttribute(chunk_tile_kernel<D, FP8, QT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<D, FP8, QT, WIDE>::SMEM);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
     const int grid = num_sms < CHUNK_MAX_CTAS ? num_sms : CHUNK_MAX_CTAS;
-    e = launch_pdl(chunk_tile_kernel<D, FP8, QT>, dim3(grid), dim3(TCfg<D, FP8, QT>::THREADS), TCfg<D, FP8, QT>::SMEM, stream, tm_q,
+    e = launch_pdl(chunk_tile_kernel<D, FP8, QT, WIDE>, dim3(grid), dim3(TCfg<D, FP8, QT, WIDE>::THREADS), TCfg<D, FP8, QT, WIDE>::SMEM, stream, tm_q,
                    tm_k, tm_v, a);
     if (e != cudaSuccess) return e;
     const int rows = a.max_q < CH_ROWS / a.g ? a.max_q * a.g : CH_ROWS;
@@ -992,8 +996,17 @@ template <int D, bool FP8>
 cudaError_t launch_tiles(const ChunkArgs& a, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                          int num_sms, cudaStream_t stream)
 {
-    return a.max_q * a.g <= CH_ROWS / 2 ? launch_typed<D, FP8, 1>(a, tm_q, tm_k, tm_v, num_sms, stream)
-                                        : launch_typed<D, FP8, 2>(a, tm_q, tm_k, tm_v, num_sms, stream);
+    if (a.max_q * a.g <= CH_ROWS / 2) return launch_typed<D, FP8, 1, 8>(a, tm_q, tm_k, tm_v, num_sms, stream);
+    if constexpr (FP8) {
+        // Eight widening warps start a piece faster; in a long one, where they wait for the softmax, four take fewer
+        // of its issue slots.  A piece has as many tiles as a sequence, or a CTA, at most.  8 / 4 warps: d = 128,
+        // 2000 tokens over 0, 2000 and 8000 rows (32 and 8 heads) 109 / 121 us, 163 / 162, 396 / 374, 64 over 16000
+        // 47.9 / 50; d = 64 (64 and 8 heads) 500 over 2000 70 / 66, 2000 over 8000 679 / 582, 300 over 0 22.4 / 23.
+        const long long seq = (static_cast<long long>(a.p.max_pages) << a.p.page_shift) / CH_KEYS;
+        const long long blocks = (static_cast<long long>(a.p.n_tokens) * a.g + CH_ROWS - 1) / CH_ROWS * a.Hk;
+        if (seq >= D / 4 && blocks * seq / num_sms >= D / 4) return launch_typed<D, FP8, 2, 4>(a, tm_q, tm_k, tm_v, num_sms, stream);
+    }
+    return launch_typed<D, FP8, 2, 8>(a, tm_q, tm_k, tm_v, num_sms, stream);
 }
 
 }  // namespace

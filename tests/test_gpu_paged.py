@@ -371,6 +371,35 @@ def test_fp8_values_of_any_size(K, n, e):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("ns,ctx,H,Hk,d", [([300, 1, 70], [200, 900, 0], 8, 2, 128), ([260, 40], [130, 1], 8, 1, 64)])
+def test_page_tables_far_wider_than_the_sequences(K, ns, ctx, H, Hk, d, fp8):
+    """Room for 256K rows a sequence; the entries past a sequence's last row are no pages."""
+    page = 64
+    cu, lens, table, n_pages = R.batch(ns, ctx, page, 240)
+    table = torch.cat([table, torch.full((len(ns), 4096 - table.shape[1]), -7, dtype=torch.int32)], 1).contiguous()
+    tensors, kd, vd = _cache(n_pages, Hk, page, d, fp8, 241)
+    q, st = _q(int(cu[-1]), H, d, 242), _status()
+    out, lse = _chunk(K, fp8, q.cuda(), *_cuda(cu, lens, table), *tensors, d ** -0.5, max_q=max(ns), dev_status=st)
+    assert int(st) == 0
+    R.check(out, lse, R.attention(q, cu, lens, table, page, kd, vd, d ** -0.5, fp16_weights=fp8), "wide tables")
+
+
+@pytest.mark.parametrize("e", [-80, 0, 80])
+def test_fp8_values_of_any_size_in_long_room(K, e):
+    """test_fp8_values_of_any_size where the sequences have room for far more rows."""
+    page, d, H, Hk, n, ctx = 64, 128, 8, 2, 150, 700
+    cu, lens, table, n_pages = R.batch([n], [ctx], page, 250)
+    table = torch.cat([table, torch.full((1, 4096 - table.shape[1]), -1, dtype=torch.int32)], 1).contiguous()
+    (kc, ks, vc, vs), kd, vd = _cache(n_pages, Hk, page, d, True, 251, spread=3.0)
+    vs *= 2.0 ** e
+    vd = vd * 2.0 ** e
+    vc[:, :, ::7], vs[:, :, ::7], vd[:, :, ::7] = 0, 0.0, 0.0
+    q = _q(n, H, d, 252, 0.3)
+    out, lse = K.attn_chunk_paged_fp8(q.cuda(), *_cuda(cu, lens, table), kc, ks, vc, vs, d ** -0.5, max_q=n)
+    R.check(out, lse, R.attention(q, cu, lens, table, page, kd, vd, d ** -0.5, fp16_weights=True), f"2^{e}")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_without_a_bound_on_the_chunks(K, fp8):
     assert _case(K, [1, 1, 1], [100, 30, 0], 8, 2, 128, 16, fp8, max_q=None) == 0
 
