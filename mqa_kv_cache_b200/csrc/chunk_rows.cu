@@ -28,6 +28,10 @@
 // eight rows of V^T's tile and the odd ones the others.  Weights enter the product as
 // 2^(s_j + log2 vs_j - m), so the values' scales cost an addition and the product's largest
 // weight is near 1 whatever they are.
+//
+// Measured (d = 128): one token each over 16 sequences of 1K - 8K rows, 32 / 8 heads, bf16 53.6 us =
+// 5.3 TB/s; over 16 of 32K rows, 64 / 8 heads, FP8 206 us = 5.4 TB/s (the loads alone, without the
+// arithmetic, 174).
 #include "common.cuh"
 #include "kernels.h"
 #include "paged.cuh"

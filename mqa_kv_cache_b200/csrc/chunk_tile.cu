@@ -25,6 +25,10 @@
 // their scores and the P V product takes them from there.  (128 keys at a time, where the
 // next scores wait for the P V that reads the weights in their place, the chain scores -
 // softmax - P V took 3960 cycles a tile against 2050 of the products alone.)
+// Measured (d = 128): 3465 and 3759 tokens behind 4096 rows, 32 / 8 heads, 592 us = 1.18 PFLOP/s
+// (680 in a stream of such calls: the power limit); bound by the MMAs' issue, as the scores' of
+// 64 keys cost what 128 would.  FP8, 1021 tokens over 31K rows, 64 heads on one KV head: 1155 us
+// = 0.91 PFLOP/s (1254); bound by the issue slots of softmax and widening.
 #include <type_traits>
 
 #include "chunk_plan.cuh"
