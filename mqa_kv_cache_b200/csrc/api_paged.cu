@@ -126,8 +126,18 @@ int encode_map(const char* name, CUtensorMap* map, const void* base, uint32_t by
 
 constexpr size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Whether a call's (sequence, KV head)s have few query rows (the row kernel's), by what the host knows.
-bool few_rows(int n_tokens, int max_q, int g) { return static_cast<long long>(max_q <= 0 || max_q > n_tokens ? n_tokens : max_q) * g <= kvattn::CHUNK_FEW_ROWS; }
+// Whether a call whose (sequence, KV head)s have up to max_q * g query rows goes to the row kernel: up to 16, or 32
+// where all the cached rows that it has room for are few, `units` sequences and KV heads times `room` of them.
+// Row / tile kernel, d = 128: 9 query rows of 16 sequences over 300, 4000 and 32000 rows (16 KV heads) 22 / 23, 86 / 91,
+// 626 / 606 us, FP8 23 / 28, 71 / 93, 416 / 575; 32 of 16 (8 KV heads) over 300, 4000 and 16000 27 / 17, 68 / 53,
+// 192 / 167, FP8 30 / 21, 75 / 61, 217 / 182; 20 of 2 (8 KV heads) over 20, 100 and 250 8.3 / 13.0, 13.2 / 13.8,
+// 13.8 / 12.9, FP8 9.3 / 15.8, 14.3 / 16.8, 14.8 / 14.8.  d = 64: 20 of 8 (2 KV heads) over 250, 500 and 1000
+// 11.0 / 12.2, 11.4 / 11.9, 14.6 / 12.7, FP8 11.6 / 14.2, 12.1 / 13.9, 16.0 / 14.6.
+long long most_rows(int n_tokens, int max_q, int g) { return static_cast<long long>(max_q <= 0 || max_q > n_tokens ? n_tokens : max_q) * g; }
+bool few_rows(long long rows, long long units, long long room, int d)
+{
+    return rows <= 16 || (rows <= kvattn::CHUNK_FEW_ROWS && units * room <= (d == 64 ? 8192 : 2048));
+}
 
 // The chunk workspace: the zero region (counters), then the partials.
 struct ChunkWorkspace {
@@ -223,7 +233,8 @@ int chunk(const char* name, bool fp8, const kvattn_bf16* q, int64_t q_stride, co
     a.d = head_dim;
     a.max_q = max_q <= 0 || max_q > n_tokens ? n_tokens : max_q;
     a.scale = scale;
-    const bool few = few_rows(n_tokens, max_q, g);
+    const bool few = few_rows(most_rows(n_tokens, max_q, g), static_cast<long long>(B) * n_kv_head,
+                              static_cast<long long>(max_pages) * page_size, head_dim);
     const ChunkWorkspace ws(few, head_dim);
     uint8_t* wp = static_cast<uint8_t*>(workspace);
     a.counters = reinterpret_cast<int*>(wp);
@@ -305,7 +316,8 @@ int kv_read_paged_fp8(const uint8_t* k_codes, const float* k_scales, const uint8
 size_t attn_chunk_paged_workspace_bytes(int B, int n_tokens, int max_q, int n_head, int n_kv_head, int head_dim)
 {
     if (B < 1 || n_head < 1 || n_kv_head < 1 || n_head % n_kv_head || head_dim < 1) return 0;
-    return ChunkWorkspace(few_rows(n_tokens, max_q, n_head / n_kv_head), head_dim).total;
+    // (either kernel may take a call of 17 to 32 query rows; the tile kernel's partials are more)
+    return ChunkWorkspace(most_rows(n_tokens, max_q, n_head / n_kv_head) <= 16, head_dim).total;
 }
 
 int attn_chunk_paged(const kvattn_bf16* q, int64_t q_stride, const int32_t* cu, const int32_t* seq_lens,

@@ -3,7 +3,7 @@
 //
 // Method: out = softmax_{j <= p} (scale q . k_j) v_j for the query at position p, query
 // head h reading KV head h / g ("注意力变体与 MoE", GQA attention(): the g heads of a
-// group share one K/V); all rows of a (sequence, KV head), its tokens times g heads, 16
+// group share one K/V); all rows of a (sequence, KV head), its tokens times g heads, 32
 // at most, meet each cached row together, so every one is read once and the kernel is
 // bound by that read.  The products run on mma.sync with the keys (then the columns of V)
 // as M and 8 query rows as N: S^T = K Q^T, O^T = V^T P^T, so that 8 rows, a group of 8
@@ -15,7 +15,7 @@
 // an unnormalised partial and the CTA that finishes last joins them, in groups of 16
 // pieces and then the groups, always in the same order.
 //
-// Four warps: 32 keys of every other tile each for all query rows, with their own running
+// Four warps per 8 or 16 query rows: 32 keys of every other tile each, with their own running
 // maximum and sum, joined at the end of a piece.  One warp loads (one box per page and 64-column
 // half, page entries fetched one tile ahead; the piece's query rows), the last one makes
 // the pieces.
@@ -55,13 +55,14 @@ struct RowPiece {
     int count;      // pieces of the unit
 };
 
-// NQ: n-tiles of 8 query rows.
-template <int D, bool FP8, int NQ>
+// NQ: n-tiles of 8 query rows in a warp; NMT: sets of four warps, each with its own such rows.
+template <int D, bool FP8, int NQ, int NMT>
 struct RCfg {
-    static constexpr int RM = 8 * NQ;  // query rows
-    static constexpr int RW = 4;       // warps that multiply
+    static constexpr int WR = 8 * NQ;      // query rows of a set of warps
+    static constexpr int RM = WR * NMT;
+    static constexpr int RW = 4 * NMT;
     static constexpr int THREADS = 32 * (RW + 2);
-    static constexpr int CTAS = FP8 ? 2 : 1;  // per SM
+    static constexpr int CTAS = FP8 && NMT == 1 ? 2 : 1;  // per SM
     static constexpr int ROWB = D * (FP8 ? 1 : 2) < 128 ? 64 : 128;  // bytes of a row of a box, and its swizzle
     static constexpr int HALVES = D * (FP8 ? 1 : 2) / ROWB;           // boxes side by side
     static constexpr int BOXD = D / HALVES;                           // columns of one
@@ -69,15 +70,15 @@ struct RCfg {
     static constexpr int TILE = HALVES * BOX;          // K or V
     static constexpr int SCB = FP8 ? 2 * RK * 4 : 0;   // their scales
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int STAGES = (FP8 ? 4 : 6) * (D == 128 ? 1 : 2);
+    static constexpr int STAGES = (FP8 ? (NMT == 1 ? 4 : 8) : (NMT == 1 ? 6 : 4)) * (D == 128 ? 1 : 2);
     static_assert(STAGES % 2 == 0, "a stage always holds even tiles or always odd ones: its barriers count one half of the warps");
     static constexpr int SCR = D + 8;                  // floats per scratch row
     static constexpr int OFF_SC = STAGES * STAGE;
     static constexpr int OFF_Q = OFF_SC + STAGES * SCB;  // two pieces' query rows
     static constexpr int QB = RM * D * 2;
-    static constexpr int OFF_O = OFF_Q + 2 * QB;         // [2][RM][SCR]
-    static constexpr int OFF_ML = OFF_O + 2 * RM * SCR * 4;  // [RW][RM] (m, l)
-    static constexpr int OFF_U = OFF_ML + RW * RM * 8;
+    static constexpr int OFF_O = OFF_Q + 2 * QB;         // [NMT][2][WR][SCR]
+    static constexpr int OFF_ML = OFF_O + 2 * RM * SCR * 4;  // [RW][WR] (m, l)
+    static constexpr int OFF_U = OFF_ML + RW * WR * 8;
     static constexpr int OFF_PIECE = OFF_U + (PAGED_MAX_B + 1) * 8;
     static constexpr int OFF_BAR = OFF_PIECE + (RPIECES * static_cast<int>(sizeof(RowPiece)) + 7) / 8 * 8;
     // full[STAGES], empty[STAGES], q_full[2], q_empty[2], piece_full[RPIECES], piece_empty[RPIECES], met
@@ -198,12 +199,12 @@ __device__ void join_pieces(const ChunkArgs& a, int gs, int f, int i0, int i1, i
     }
 }
 
-template <int D, bool FP8, int NQ>
-__global__ void __launch_bounds__(RCfg<D, FP8, NQ>::THREADS, RCfg<D, FP8, NQ>::CTAS)
+template <int D, bool FP8, int NQ, int NMT>
+__global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, NQ, NMT>::CTAS)
     chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, ChunkArgs a)
 {
-    using C = RCfg<D, FP8, NQ>;
-    constexpr int KS = D / 16, STAGES = C::STAGES, RM = C::RM, RW = C::RW;
+    using C = RCfg<D, FP8, NQ, NMT>;
+    constexpr int KS = D / 16, STAGES = C::STAGES, RM = C::RM, RW = C::RW, WR = C::WR;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (stays a shared-memory address to the compiler)
     float* s_o = reinterpret_cast<float*>(smem + C::OFF_O);
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ>::THREADS, RCfg<D, FP8, NQ>::C
 
     // ===== consumers =====
     const int r0 = lane >> 2, cq = lane & 3;
-    const int sub = warp;
+    const int mt = warp >> 2, sub = warp & 3;
     const uint32_t turn = sub >> 1;   // even or odd tiles
     const int tok0 = (sub & 1) * 32;  // this warp's keys of a tile
     const int mi = lane >> 3, rr = lane & 7;
@@ -450,13 +451,13 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ>::THREADS, RCfg<D, FP8, NQ>::C
             const uint8_t* sq = smem + C::OFF_Q + (np & 1) * C::QB;
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                const int row = n * 8 + r0;
+                const int row = mt * WR + n * 8 + r0;
                 const bool v = have && row < rows;
                 const uint8_t* qr = sq + row * D * 2;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     qs[n][e] = sl2;
-                    pos[n][e] = pc.pos0 + ((n * 8 + 2 * cq + e) >> gs);
+                    pos[n][e] = pc.pos0 + ((mt * WR + n * 8 + 2 * cq + e) >> gs);
                 }
                 if constexpr (FP8) {
                     // k step x of thread cq: columns (D / 4) cq + 4 x + {0, 1 | 2, 3}
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ>::THREADS, RCfg<D, FP8, NQ>::C
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_empty[np & 1]);
         }
-        const int pos_min = pc.pos0;
+        const int pos_min = pc.pos0 + ((mt * WR) >> gs);
         float o[NQ][D / 16][4];  // O^T: 16 columns of V, 8 query rows
         float m[NQ][2], l[NQ][2];
 #pragma unroll
@@ -695,20 +696,20 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ>::THREADS, RCfg<D, FP8, NQ>::C
                 l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
                 l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
                 l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
-                if (r0 == 0) s_ml[warp * RM + n * 8 + 2 * cq + e] = make_float2(m[n][e], l[n][e]);
+                if (r0 == 0) s_ml[warp * WR + n * 8 + 2 * cq + e] = make_float2(m[n][e], l[n][e]);
             }
         meet();
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float2* ml = s_ml + n * 8 + 2 * cq + e;
+                const float2* ml = s_ml + mt * 4 * WR + n * 8 + 2 * cq + e;
                 float M = -INFINITY, L = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) M = fmaxf(M, ml[j * RM].x);
+                for (int j = 0; j < 4; ++j) M = fmaxf(M, ml[j * WR].x);
                 const float mu = M == -INFINITY ? 0.f : M;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) L += sum_exp2(ml[j * RM].y, ml[j * RM].x - mu);
+                for (int j = 0; j < 4; ++j) L += sum_exp2(ml[j * WR].y, ml[j * WR].x - mu);
                 const float w = fast_exp2(m[n][e] - mu);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ>::THREADS, RCfg<D, FP8, NQ>::C
             }
         // (query row, first column, and the step to the second one) of o[n][i][e] and o[n][i][2 + e]
         constexpr int CS = FP8 ? 1 : 8;
-        float* so = s_o + (sub & 1) * RM * C::SCR + 2 * cq * C::SCR + (FP8 ? 2 * r0 : r0);
+        float* so = s_o + (mt * 2 + (sub & 1)) * WR * C::SCR + 2 * cq * C::SCR + (FP8 ? 2 * r0 : r0);
         if (sub >= 2) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
@@ -742,17 +743,17 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ>::THREADS, RCfg<D, FP8, NQ>::C
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) s_ml[warp * RM + n * 8 + 2 * cq + e] = make_float2(m[n][e], l[n][e]);
+                for (int e = 0; e < 2; ++e) s_ml[warp * WR + n * 8 + 2 * cq + e] = make_float2(m[n][e], l[n][e]);
         }
         meet();
         // ---- the rows: finished, or a partial ----
         const long long slot = static_cast<long long>(2 * c + (c == pc.first ? 1 : 0)) * RM;
         for (int idx = threadIdx.x; idx < rows * (D / 4); idx += RW * 32) {
             const int r = idx / (D / 4), q4 = idx - r * (D / 4);
-            const float* sr = s_o + r * C::SCR + 4 * q4;
-            const float4 x = *reinterpret_cast<const float4*>(sr), y = *reinterpret_cast<const float4*>(sr + RM * C::SCR);
+            const float* sr = s_o + ((r / WR) * 2 * WR + r % WR) * C::SCR + 4 * q4;
+            const float4 x = *reinterpret_cast<const float4*>(sr), y = *reinterpret_cast<const float4*>(sr + WR * C::SCR);
             const float4 v = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-            const float2 ml = s_ml[r];
+            const float2 ml = s_ml[(r / WR) * 4 * WR + r % WR];
             if (pc.count == 1) {
                 const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
                 const long long row = static_cast<long long>(pc.t0 + (r >> gs)) * a.H + static_cast<long long>(pc.kvh) * a.g + (r & (a.g - 1));
@@ -819,31 +820,33 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ>::THREADS, RCfg<D, FP8, NQ>::C
     }
 }
 
-template <int D, bool FP8, int NQ>
+template <int D, bool FP8, int NQ, int NMT>
 cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
                          cudaStream_t stream)
 {
-    using C = RCfg<D, FP8, NQ>;
+    using C = RCfg<D, FP8, NQ, NMT>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(chunk_rows_kernel<D, FP8, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        e = cudaFuncSetAttribute(chunk_rows_kernel<D, FP8, NQ, NMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
     int grid = num_sms * C::CTAS;
     if (grid > CHUNK_MAX_SLOTS) grid = CHUNK_MAX_SLOTS;
-    return launch_pdl(chunk_rows_kernel<D, FP8, NQ>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tm_k, tm_v, a);
+    return launch_pdl(chunk_rows_kernel<D, FP8, NQ, NMT>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tm_k, tm_v, a);
 }
 
 template <int D, bool FP8>
 cudaError_t launch_rows(const ChunkArgs& a, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
                         cudaStream_t stream)
 {
-    return a.max_q * a.g <= 8 ? launch_typed<D, FP8, 1>(a, tm_k, tm_v, num_sms, stream)
-                              : launch_typed<D, FP8, 2>(a, tm_k, tm_v, num_sms, stream);
+    const int rows = a.max_q * a.g;
+    return rows <= 8    ? launch_typed<D, FP8, 1, 1>(a, tm_k, tm_v, num_sms, stream)
+           : rows <= 16 ? launch_typed<D, FP8, 2, 1>(a, tm_k, tm_v, num_sms, stream)
+                        : launch_typed<D, FP8, 2, 2>(a, tm_k, tm_v, num_sms, stream);
 }
 
 }  // namespace

@@ -72,10 +72,7 @@ struct ChunkArgs {
 };
 constexpr int CHUNK_MAX_CTAS = 148;     // tile kernel: at most this many CTAs, with slots of 256 rows
 constexpr int CHUNK_SLOT_ROWS = 256;
-// Row kernel: query rows of a (sequence, KV head), and of a slot, at most.  Row / tile kernel, 16 sequences of 300, 4000 and
-// 16000 rows (8 KV heads): 32 query rows 27 / 17, 68 / 53, 192 / 167 us, FP8 30 / 21, 75 / 61, 217 / 182; of 300, 4000 and
-// 32000 rows (16 KV heads), 9 query rows 22 / 23, 86 / 91, 626 / 606, FP8 23 / 28, 71 / 93, 416 / 575.
-constexpr int CHUNK_FEW_ROWS = 16;
+constexpr int CHUNK_FEW_ROWS = 32;      // row kernel: query rows of a (sequence, KV head), and of a slot, at most
 constexpr int CHUNK_MAX_SLOTS = 296;    // row kernel: at most this many CTAs
 static_assert(3 * CHUNK_MAX_SLOTS * 4 <= KVATTN_DECODE_WS_ZERO_BYTES, "counters");
 cudaError_t launch_chunk_rows(const ChunkArgs& a, bool fp8, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
