@@ -12,8 +12,8 @@
 // Work: the 64-key tiles of all (sequence, KV head) units form one line, dealt out to the
 // CTAs in equal stretches (as decode_plan.cuh does for contiguous caches); a stretch of a
 // unit is a piece.  A unit in one piece is finished at once; otherwise each piece leaves
-// an unnormalised partial and the CTA that finishes last joins them, in groups of 16
-// pieces and then the groups, always in the same order.
+// an unnormalised partial and the CTA that finishes last joins them (up to 32 at once, more
+// in groups of 16 and then the groups), always in the same order.
 //
 // Four warps per 8 or 16 query rows: 32 keys of every other tile each, with their own running
 // maximum and sum, joined at the end of a piece.  One warp loads (one box per page and 64-column
@@ -29,8 +29,8 @@
 // 2^(s_j + log2 vs_j - m), so the values' scales cost an addition and the product's largest
 // weight is near 1 whatever they are.
 //
-// Measured (d = 128): one token each over 16 sequences of 1K - 8K rows, 32 / 8 heads, bf16 53.6 us =
-// 5.3 TB/s; over 16 of 32K rows, 64 / 8 heads, FP8 206 us = 5.4 TB/s (the loads alone, without the
+// Measured (d = 128): one token each over 16 sequences of 1K - 8K rows, 32 / 8 heads, bf16 51.6 us =
+// 5.5 TB/s; over 16 of 32K rows, 64 / 8 heads, FP8 204 us = 5.4 TB/s (the loads alone, without the
 // arithmetic, 174).
 #include "common.cuh"
 #include "kernels.h"
