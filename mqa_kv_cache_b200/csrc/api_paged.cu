@@ -126,17 +126,22 @@ int encode_map(const char* name, CUtensorMap* map, const void* base, uint32_t by
 
 constexpr size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Whether a call whose (sequence, KV head)s have up to max_q * g query rows goes to the row kernel: up to 16, or 32
-// where all the cached rows that it has room for are few, `units` sequences and KV heads times `room` of them.
+// Whether a call whose (sequence, KV head)s have up to max_q * g query rows goes to the row kernel: up to 8; 16 where
+// the units, sequences times KV heads, are not shared by many CTAs each (as the last one of those joins a unit's rows);
+// 32 where all the cached rows that it has room for are few, `units` times `room` of them.
 // Row / tile kernel, d = 128: 9 query rows of 16 sequences over 300, 4000 and 32000 rows (16 KV heads) 22 / 23, 86 / 91,
 // 626 / 606 us, FP8 23 / 28, 71 / 93, 416 / 575; 32 of 16 (8 KV heads) over 300, 4000 and 16000 27 / 17, 68 / 53,
 // 192 / 167, FP8 30 / 21, 75 / 61, 217 / 182; 20 of 2 (8 KV heads) over 20, 100 and 250 8.3 / 13.0, 13.2 / 13.8,
 // 13.8 / 12.9, FP8 9.3 / 15.8, 14.3 / 16.8, 14.8 / 14.8.  d = 64: 20 of 8 (2 KV heads) over 250, 500 and 1000
-// 11.0 / 12.2, 11.4 / 11.9, 14.6 / 12.7, FP8 11.6 / 14.2, 12.1 / 13.9, 16.0 / 14.6.
+// 11.0 / 12.2, 11.4 / 11.9, 14.6 / 12.7, FP8 11.6 / 14.2, 12.1 / 13.9, 16.0 / 14.6.  16 query rows of 2 (4 KV heads) over
+// 300, 1000 and 4000, d = 128: 12.4 / 12.8, 14.4 / 11.7, 22.1 / 13.8, FP8 15.5 / 15.5, 17.7 / 14.2, 23.7 / 16.3; d = 64, 8
+// sequences of one KV head: 9.8 / 11.9, 11.0 / 11.6, 15.9 / 15.0.
 long long most_rows(int n_tokens, int max_q, int g) { return static_cast<long long>(max_q <= 0 || max_q > n_tokens ? n_tokens : max_q) * g; }
 bool few_rows(long long rows, long long units, long long room, int d)
 {
-    return rows <= 16 || (rows <= kvattn::CHUNK_FEW_ROWS && units * room <= (d == 64 ? 8192 : 2048));
+    if (rows <= 8) return true;
+    if (rows <= 16) return d == 64 || units > 16 || room < 1024;
+    return rows <= kvattn::CHUNK_FEW_ROWS && units * room <= (d == 64 ? 8192 : 2048);
 }
 
 // The chunk workspace: the zero region (counters), then the partials.
@@ -316,8 +321,9 @@ int kv_read_paged_fp8(const uint8_t* k_codes, const float* k_scales, const uint8
 size_t attn_chunk_paged_workspace_bytes(int B, int n_tokens, int max_q, int n_head, int n_kv_head, int head_dim)
 {
     if (B < 1 || n_head < 1 || n_kv_head < 1 || n_head % n_kv_head || head_dim < 1) return 0;
-    // (either kernel may take a call of 17 to 32 query rows; the tile kernel's partials are more)
-    return ChunkWorkspace(most_rows(n_tokens, max_q, n_head / n_kv_head) <= 16, head_dim).total;
+    // (where either kernel may take the call, by its room: the tile kernel's partials are more)
+    const long long rows = most_rows(n_tokens, max_q, n_head / n_kv_head);
+    return ChunkWorkspace(rows <= 8 || (rows <= 16 && (head_dim == 64 || static_cast<long long>(B) * n_kv_head > 16)), head_dim).total;
 }
 
 int attn_chunk_paged(const kvattn_bf16* q, int64_t q_stride, const int32_t* cu, const int32_t* seq_lens,

@@ -470,6 +470,12 @@ def test_blocks_shared_by_many_ctas(K, ns, ctx, H, Hk, d, fp8):
     assert _case(K, ns, ctx, H, Hk, d, 64, fp8, seed=45, max_q=max(ns), poison=False) == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("ns,ctx,H,Hk,d", [([2, 2, 1], [1500, 700, 40], 64, 8, 128), ([2, 1], [5000, 900], 16, 2, 64)])
+def test_sixteen_rows_a_head_shared_by_ctas(K, ns, ctx, H, Hk, d, fp8):
+    assert _case(K, ns, ctx, H, Hk, d, 64, fp8, seed=260, max_q=2) == 0
+
+
 def test_many_sequences(K):
     ns = [1 + (b % 3) for b in range(300)]
     ctx = [(b * 37) % 150 for b in range(300)]
