@@ -96,8 +96,11 @@ struct TCfg {
     static constexpr int OFF_CU = OFF_U + (PAGED_MAX_B + 1) * 8;
     static constexpr int OFF_LEN = OFF_CU + (PAGED_MAX_B + 1) * 4;
     static constexpr int OFF_ML = (OFF_LEN + PAGED_MAX_B * 4 + 15) / 16 * 16;  // [2][128] (max, sum)
-    static constexpr int OFF_QS = OFF_ML + 2 * 128 * 8;  // [2 pieces][256] powers of two that Q's rows were divided by (FP8)
-    static constexpr int OFF_PIECE = OFF_QS + (FP8 ? 2 * CH_ROWS * 4 : 0);
+    // [PIECES][256] exponents of the powers of two that Q's rows were multiplied by (FP8).  A place per piece of the
+    // ring: Q may be widened for a piece while a softmax warp still has to read them for the second or third one
+    // before it; piece_empty, which every softmax warp releases when it is through with a piece, orders the reuse
+    static constexpr int OFF_QS = OFF_ML + 2 * 128 * 8;
+    static constexpr int OFF_PIECE = OFF_QS + (FP8 ? PIECES * CH_ROWS * 2 : 0);
     static constexpr int OFF_BAR = OFF_PIECE + PIECES * static_cast<int>(sizeof(Piece));
     // kv_full[NS], kv_empty[NS], land_full[LS], land_empty[LS], q_full, q_empty, s_full[4], p_full[4], pv_done[4],
     // joined[2], piece_full[PIECES], piece_empty[PIECES], done, q_ready
@@ -125,6 +128,12 @@ __device__ __forceinline__ float lg2(float x)
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 2^-up for an exponent of -253 .. 252, in two factors as one alone may leave fp32's range.
+__device__ __forceinline__ float pow2_neg(int up)
+{
+    return __int_as_float((127 - (up >> 1)) << 23) * __int_as_float((127 - up + (up >> 1)) << 23);
 }
 
 // Two weights, as the MMAs take them.
@@ -233,7 +242,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT, WIDE>::THREADS, 1)
     uint64_t* piece_empty = piece_full + PIECES;
     uint64_t* done = piece_empty + PIECES;
     uint64_t* q_ready = done + 1;  // FP8: Q's rows are fp16
-    float* s_qs = reinterpret_cast<float*>(smem + C::OFF_QS);
+    int16_t* s_qs = reinterpret_cast<int16_t*>(smem + C::OFF_QS);
     const Piece* s_piece = reinterpret_cast<const Piece*>(smem + C::OFF_PIECE);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -533,11 +542,11 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT, WIDE>::THREADS, 1)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 if (FP8 && k == 0) {  // (the scores wait for the converted Q rows)
-                    const float* qs = s_qs + (n & 1) * CH_ROWS + row0 + (lane >> 2);
+                    const int16_t* qs = s_qs + (n % PIECES) * CH_ROWS + row0 + (lane >> 2);
                     // not 0, as that times the -inf of a key out of sight is no number (a tiny or zero row: its
                     // scores are 0 either way)
-                    sl2a = fmaxf(sl2 * qs[0], 0x1p-126f);
-                    sl2b = fmaxf(sl2 * qs[8], 0x1p-126f);
+                    sl2a = fmaxf(sl2 * pow2_neg(qs[0]), 0x1p-126f);
+                    sl2b = fmaxf(sl2 * pow2_neg(qs[8]), 0x1p-126f);
                 }
                 if (active_warp) {
                     const uint32_t bad = s_bad[it % C::RING] >> (4 * hh) & 15u;
@@ -795,7 +804,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT, WIDE>::THREADS, 1)
                     for (int e = 0; e < 4; ++e)
                         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[e]) : "f"(bf16_hi(w[e]) * fa * fb), "f"(bf16_lo(w[e]) * fa * fb));
                     *q = make_uint4(o[0], o[1], o[2], o[3]);
-                    if (c8 == 0) s_qs[(n & 1) * CH_ROWS + row] = __int_as_float((127 - (up >> 1)) << 23) * __int_as_float((127 - up + (up >> 1)) << 23);
+                    if (c8 == 0) s_qs[(n % PIECES) * CH_ROWS + row] = static_cast<int16_t>(up);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
