@@ -26,8 +26,9 @@
 // 2^-29 of its row's largest rounds to a multiple of 2^-40 of it, far below the fp32 sums'
 // own rounding).  V: transposed as pairs of bytes, the even columns of 16 being the first
 // eight rows of V^T's tile and the odd ones the others.  Weights enter the product as
-// 2^(s_j + log2 vs_j - m), so the values' scales cost an addition and the product's largest
-// weight is near 1 whatever they are.
+// 2^(14 + s_j + log2 vs_j - m), so the values' scales cost an addition and the product's largest
+// weight is near 2^14 whatever they are: what is below 2^-39 of it is lost to fp16 (from 2^-25 on if it stood
+// at 1, and 16K such weights of 2^-25 are 2^-11 of the sum).
 //
 // Measured (d = 128): one token each over 16 sequences of 1K - 8K rows, 32 / 8 heads, bf16 51.6 us =
 // 5.5 TB/s; over 16 of 32K rows, 64 / 8 heads, FP8 204 us = 5.4 TB/s (the loads alone, without the
@@ -43,6 +44,7 @@ namespace {
 constexpr int RK = 64;        // keys per tile
 constexpr int RBATCH = 16;    // partials requested together
 constexpr int RPIECES = 4;    // pieces handed out ahead
+constexpr float kWeightLog2 = 14.f;  // FP8: the largest weight of the product, in log2 units
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -613,6 +615,12 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
                     }
                 }
                 // ---- P^T ----
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) lv[i][e] += kWeightLog2;
+                }
                 uint32_t pb[NQ][2][2];
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
@@ -710,7 +718,7 @@ __global__ void __launch_bounds__(RCfg<D, FP8, NQ, NMT>::THREADS, RCfg<D, FP8, N
                 const float mu = M == -INFINITY ? 0.f : M;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) L += sum_exp2(ml[j * WR].y, ml[j * WR].x - mu);
-                const float w = fast_exp2(m[n][e] - mu);
+                const float w = fast_exp2(m[n][e] - mu - (FP8 ? kWeightLog2 : 0.f));
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     o[n][i][e] *= w;

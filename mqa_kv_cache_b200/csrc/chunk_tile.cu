@@ -41,9 +41,12 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-// log2 units: the maximum moves only when it grows by more than this (FP8 weights of up to 2^12 fit fp16; at 8, where
-// the values' scales moved it more often, 16 x 8 tokens over 8K rows took 110 us instead of 107)
+// log2 units: the maximum moves only when it grows by more than this (at 8, where the values' scales moved it more
+// often, 16 x 8 tokens over 8K rows took 110 us instead of 107)
 constexpr float kRescaleThreshold = 12.0f;
+// FP8: weights times the values' scales enter the product times this, up to 2^15 then, what fp16 has room for: a
+// weight is lost below 2^-28 of the largest (2^-25 without it, a sum of which reaches 2^-11 over 16K rows)
+constexpr float kWeightScale = 8.0f;
 
 // A stretch of one unit's key tiles, as warp 19 hands it to the others (rows = 0: no more).
 struct Piece {
@@ -91,7 +94,7 @@ struct TCfg {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_KV = QT * TILE;
     static constexpr int OFF_LAND = OFF_KV + NS * TILE;
-    static constexpr int OFF_SC = OFF_LAND + LS * CODES;  // [RING][3][128]: K's scales; V's, as log2; V's
+    static constexpr int OFF_SC = OFF_LAND + LS * CODES;  // [RING][3][128]: K's scales; V's, as log2; V's times kWeightScale
     static constexpr int OFF_U = OFF_SC + (FP8 ? RING * 3 * CH_KEYS * 4 : 0);
     static constexpr int OFF_CU = OFF_U + (PAGED_MAX_B + 1) * 8;
     static constexpr int OFF_LEN = OFF_CU + (PAGED_MAX_B + 1) * 4;
@@ -674,7 +677,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT, WIDE>::THREADS, 1)
             tc_fence_after();
             // ---- the piece's rows: finished, or a partial for the merge ----
             float va = 0.f, vb = 0.f;  // weights of the other buffer's sums; ua, ub of this one's (nothing seen: 0, as
-            float ua = ma == -INFINITY ? 0.f : 1.f, ub = mb == -INFINITY ? 0.f : 1.f;  // it may never have been written)
+            constexpr float UNIT = FP8 ? 1.f / kWeightScale : 1.f;
+            float ua = ma == -INFINITY ? 0.f : UNIT, ub = mb == -INFINITY ? 0.f : UNIT;  // it may never have been written)
             int c0 = 0, c1 = D / 16;   // column pieces of 16
             if (!pair) {
                 // join the two buffers: each group writes half of the columns
@@ -690,10 +694,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT, WIDE>::THREADS, 1)
                 const float2 oa = s_ml[(t ^ 1) * 128 + r16 + (lane >> 2)], ob = s_ml[(t ^ 1) * 128 + r16 + (lane >> 2) + 8];
                 const float Ma = fmaxf(ma, oa.x), Mb = fmaxf(mb, ob.x);
                 const float fa = Ma == -INFINITY ? 0.f : Ma, fb = Mb == -INFINITY ? 0.f : Mb;
-                ua = fast_exp2(ma - fa);
-                ub = fast_exp2(mb - fb);
-                va = fast_exp2(oa.x - fa);
-                vb = fast_exp2(ob.x - fb);
+                ua = fast_exp2(ma - fa) * UNIT;
+                ub = fast_exp2(mb - fb) * UNIT;
+                va = fast_exp2(oa.x - fa) * UNIT;
+                vb = fast_exp2(ob.x - fb) * UNIT;
                 la = sum_exp2(la, ma - fa) + sum_exp2(oa.y, oa.x - fa);
                 lb = sum_exp2(lb, mb - fb) + sum_exp2(ob.y, ob.x - fb);
                 ma = Ma;
@@ -769,7 +773,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT, WIDE>::THREADS, 1)
             // fp16 is one conversion for two codes, exact, and three more bits of the weights than bf16 (the long
             // chunk's outputs are off by 0.0017 of their norm, their own rounding, where bf16 weights gave 0.0025).
             // Its range is enough: Q's rows are scaled into it, and a row's running reference is the maximum of
-            // s + log2 vs over the keys it sees, so its weights times the values' scales stay below 2^12 (and the largest above 1).
+            // s + log2 vs over the keys it sees, so its weights times the values' scales stay below 2^12 (and the largest above 1),
+            // below 2^15 with kWeightScale.
             const int tid = threadIdx.x - 640, cwarp = tid >> 5;
             // chunk of 16 codes: two rows by four chunks in eight neighbouring lanes, so that either half of their
             // 32 bytes falls on eight different bank groups
@@ -828,6 +833,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT, WIDE>::THREADS, 1)
                                 lv = 0.f;
                             }
                             sc[CH_KEYS] = lv;
+                            sc[2 * CH_KEYS] *= kWeightScale;
                         }
                         const uint8_t* src = smem + C::OFF_LAND + ls * C::CODES;
                         uint8_t* dst = smem + C::OFF_KV + slot * C::TILE + (ch >> 2) * C::BOX;
