@@ -477,7 +477,8 @@ int attn_decode_sparse_fp8(const kvattn_bf16* q, const uint8_t* latent_fp8, cons
  * bf16: k_pages, v_pages [n_pages][n_kv_head][page_size][d].  FP8: codes uint8
  * [n_pages][n_kv_head][page_size][d] and one fp32 scale per row and head
  * [n_pages][n_kv_head][page_size], d + 4 bytes for a row of K or V; a row stands for
- * code * scale, quantised by the rule of the FP8 section above (one group of d values).
+ * code * scale, quantised by the rule of the FP8 section above (one group of d values):
+ * scales are finite and not negative, codes of rows in use are numbers.
  * Device-side checks.  cu outside 0 .. n_tokens or decreasing, or a length outside
  * [0, max_pages * page_size]: forced into range, KVATTN_STATUS_BAD_LENGTH.  A needed page
  * outside [0, n_pages): its rows are skipped, KVATTN_STATUS_BAD_INDEX.  Sequences that
@@ -530,8 +531,10 @@ int kv_read_paged_fp8(const uint8_t* k_codes, const float* k_scales, const uint8
  * gets out = 0 and lse = -inf.  Rows past a sequence's length are never used, whatever they
  * hold; its own rows must be finite (a non-finite value row can reach the queries that
  * share a key tile with it).
- * max_q: an upper bound of the chunk lengths that the host knows (<= 0: n_tokens); it
- * decides how the work is laid out.  A chunk longer than max_q sets
+ * max_q: an upper bound of the chunk lengths that the host knows (<= 0: n_tokens).  With the
+ * room of the page table (max_pages * page_size, taken for the sequences' length) it decides
+ * how the work is laid out (results differ by rounding): a batch of single tokens without its
+ * bound of 1 is laid out as for chunks of n_tokens, and slower.  A chunk longer than max_q sets
  * KVATTN_STATUS_BAD_LENGTH and its tokens from max_q on are left unwritten.
  * workspace: attn_chunk_paged_workspace_bytes(...) bytes for the same B, n_tokens, max_q
  * and heads, 256-byte aligned; its first KVATTN_DECODE_WS_ZERO_BYTES must be zero before
@@ -543,7 +546,9 @@ int kv_read_paged_fp8(const uint8_t* k_codes, const float* k_scales, const uint8
  * the dequantised rows are never rounded.  The weights times the values' scales are rounded
  * once, to fp16 (over a bf16 cache to bf16), and the sums take them unrounded: over n rows a
  * value is off by at most n 2^-28 of the largest weighted row beside the relative 2^-11 (few
- * query rows per KV head: n 2^-39).
+ * query rows per KV head: n 2^-39).  The cache is half the size; in time, calls of up
+ * to 16 query rows (n g) per KV head gain by it over long caches, and from 17 on the bf16 cache is the
+ * faster one.
  */
 size_t attn_chunk_paged_workspace_bytes(int B, int n_tokens, int max_q, int n_head, int n_kv_head, int head_dim);
 

@@ -22,9 +22,9 @@
 //
 // FP8: the codes become fp16 in registers, one conversion for two of them (exact).  K: a
 // thread's codes of a key are 16-byte loads, the k order of the MMA being free as long as Q
-// follows it; Q is scaled per row by a power of two into fp16's range (an element below
-// 2^-29 of its row's largest rounds to a multiple of 2^-40 of it, far below the fp32 sums'
-// own rounding).  V: transposed as pairs of bytes, the even columns of 16 being the first
+// follows it; Q is scaled per row by a power of two into fp16's range, its largest element to
+// [2^14, 2^15) (bf16's eight bits are exact there down to 2^-31 of it; a smaller element rounds
+// to a multiple of at most 2^-38 of it, far below the fp32 sums' own rounding).  V: transposed as pairs of bytes, the even columns of 16 being the first
 // eight rows of V^T's tile and the odd ones the others.  Weights enter the product as
 // 2^(14 + s_j + log2 vs_j - m), so the values' scales cost an addition and the product's largest
 // weight is near 2^14 whatever they are: what is below 2^-39 of it is lost to fp16 (from 2^-25 on if it stood

@@ -28,7 +28,8 @@
 // Measured (d = 128): 3465 and 3759 tokens behind 4096 rows, 32 / 8 heads, 592 us = 1.18 PFLOP/s
 // (680 in a stream of such calls: the power limit); bound by the MMAs' issue, as the scores' of
 // 64 keys cost what 128 would.  FP8, 1021 tokens over 31K rows, 64 heads on one KV head: 1155 us
-// = 0.91 PFLOP/s (1254); bound by the issue slots of softmax and widening.
+// = 0.91 PFLOP/s (1254 to 1274); no unit is near its limit (tcgen05 pipe 56%, issue slots 64%): the
+// dependent steps widening - scores - softmax - P V set the pace.
 #include <type_traits>
 
 #include "chunk_plan.cuh"
@@ -800,8 +801,8 @@ __global__ void __launch_bounds__(TCfg<D, FP8, QT, WIDE>::THREADS, 1)
 #pragma unroll
                     for (int o = D / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                     // largest element to [2^14, 2^15), by its exponent field (0 of a zero or subnormal row: taken as
-                    // 1): an element below 2^-29 of the largest rounds to a multiple of 2^-40 of it, far below the
-                    // fp32 sums' own rounding.  Two factors, as one may leave fp32's range: 2^(141 - e) = fa fb.
+                    // 1): exact down to 2^-31 of the largest (bf16's eight bits, steps of 2^-24 in fp16), below that
+                    // rounded to a multiple of at most 2^-38 of it, far below the fp32 sums' own rounding.  Two factors, as one may leave fp32's range: 2^(141 - e) = fa fb.
                     const int e8 = max(static_cast<int>(__float_as_uint(m) >> 23), 1), up = 141 - e8;
                     const float fa = __int_as_float((127 + (up >> 1)) << 23), fb = __int_as_float((127 + up - (up >> 1)) << 23);
                     uint32_t o[4];

@@ -880,13 +880,15 @@ def attn_chunk_paged(q, cu, seq_lens, page_table, k_pages, v_pages, scale, max_q
     bf16 cache that already holds the new tokens' rows: q [n_tokens, H, d] (rotated by the caller),
     cu int32 [B + 1], seq_lens int32 [B] (rows with the new tokens), page_table int32
     [B, max_pages], pages [n_pages, Hk, page, d] -> (out [n_tokens, H, d] bf16, lse [n_tokens, H]
-    fp32 or None).  max_q: an upper bound of the chunk lengths known to the host."""
+    fp32 or None).  max_q: an upper bound of the chunk lengths known to the host; without it the
+    work is laid out as for chunks of n_tokens, which is slower for a batch of single tokens (give 1)."""
     return _chunk_paged(_lib.attn_chunk_paged, False, q, cu, seq_lens, page_table, k_pages, None, v_pages, None, scale,
                         max_q, out, lse, ws, dev_status, want_lse)
 
 
 def attn_chunk_paged_fp8(q, cu, seq_lens, page_table, k_codes, k_scales, v_codes, v_scales, scale, max_q=None,
                          out=None, lse=None, ws=None, dev_status=None, want_lse=True):
-    """attn_chunk_paged over an FP8 cache (kv_append_paged_rope_fp8)."""
+    """attn_chunk_paged over an FP8 cache (kv_append_paged_rope_fp8): faster than over a bf16 cache for up to
+    16 query rows per KV head and long sequences, slower from 17 on."""
     return _chunk_paged(_lib.attn_chunk_paged_fp8, True, q, cu, seq_lens, page_table, k_codes, k_scales, v_codes,
                         v_scales, scale, max_q, out, lse, ws, dev_status, want_lse)
