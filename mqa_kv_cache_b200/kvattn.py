@@ -881,7 +881,9 @@ def attn_chunk_paged(q, cu, seq_lens, page_table, k_pages, v_pages, scale, max_q
     cu int32 [B + 1], seq_lens int32 [B] (rows with the new tokens), page_table int32
     [B, max_pages], pages [n_pages, Hk, page, d] -> (out [n_tokens, H, d] bf16, lse [n_tokens, H]
     fp32 or None).  max_q: an upper bound of the chunk lengths known to the host; without it the
-    work is laid out as for chunks of n_tokens, which is slower for a batch of single tokens (give 1)."""
+    work is laid out as for chunks of n_tokens, which is slower for a batch of single tokens (give 1).
+    ws: workspace(attn_chunk_paged_workspace_bytes(...)), kept between calls; without it every call makes and
+    zeroes one (up to 39 MB)."""
     return _chunk_paged(_lib.attn_chunk_paged, False, q, cu, seq_lens, page_table, k_pages, None, v_pages, None, scale,
                         max_q, out, lse, ws, dev_status, want_lse)
 
