@@ -478,7 +478,8 @@ int attn_decode_sparse_fp8(const kvattn_bf16* q, const uint8_t* latent_fp8, cons
  * [n_pages][n_kv_head][page_size][d] and one fp32 scale per row and head
  * [n_pages][n_kv_head][page_size], d + 4 bytes for a row of K or V; a row stands for
  * code * scale, quantised by the rule of the FP8 section above (one group of d values):
- * scales are finite and not negative, codes of rows in use are numbers.
+ * scales lie in 0 .. 2^120 (the largest bf16 value over 448 does), codes of rows in use are
+ * numbers.
  * Device-side checks.  cu outside 0 .. n_tokens or decreasing, or a length outside
  * [0, max_pages * page_size]: forced into range, KVATTN_STATUS_BAD_LENGTH.  A needed page
  * outside [0, n_pages): its rows are skipped, KVATTN_STATUS_BAD_INDEX.  Sequences that
